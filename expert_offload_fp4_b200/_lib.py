@@ -18,6 +18,8 @@ MOE_COPY_SM, MOE_COPY_DMA = 0, 1
 MOE_BW_PCIE, MOE_BW_HOST = 0, 1
 STATUS_READY_TIMEOUT, STATUS_DEP_TIMEOUT, STATUS_BAD_SLOT, STATUS_BAD_EXPERT, STATUS_PIPE_TIMEOUT = 1, 2, 4, 8, 16
 STATUS_NOT_RESIDENT = 32
+MOE_BF16, MOE_F32 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
 class MoeConfig(C.Structure):
@@ -46,6 +48,16 @@ class BwEstimate(C.Structure):
                 ("n_pcie", C.c_longlong), ("n_host", C.c_longlong)]
 
 
+class RouteChoice(C.Structure):
+    _fields_ = [("k", C.c_int), ("score", C.c_int), ("n_group", C.c_int), ("topk_group", C.c_int),
+                ("group_top", C.c_int), ("renormalize", C.c_int), ("scale", C.c_float)]
+
+
+class Fp4WeightDesc(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("tensor_scale", C.c_float),
+                ("N", C.c_int), ("K", C.c_int), ("fmt", C.c_int)]
+
+
 class Stats(C.Structure):
     _fields_ = [("lookups", C.c_longlong), ("unique", C.c_longlong), ("hits", C.c_longlong),
                 ("misses", C.c_longlong), ("evictions", C.c_longlong),
@@ -59,7 +71,7 @@ class MoeError(RuntimeError):
 
 
 # name -> (restype, argtypes); every entry point of include/moe_fp4.h
-vp, i32, f64, sz = C.c_void_p, C.c_int, C.c_double, C.c_size_t
+vp, i32, i64, f64, sz = C.c_void_p, C.c_int, C.c_longlong, C.c_double, C.c_size_t
 SIGNATURES = {
     "moe_last_error": (C.c_char_p, []),
     "moe_pool_create": (i32, [C.POINTER(MoeConfig), C.POINTER(vp)]),
@@ -72,6 +84,12 @@ SIGNATURES = {
     "moe_pool_slot_ptr": (i32, [vp, i32, C.POINTER(vp), C.POINTER(sz)]),
     "moe_route_workspace_bytes": (sz, [i32, i32]),
     "moe_route": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+    "moe_route_grouped_workspace_bytes": (sz, [i32, i32]),
+    "moe_route_grouped": (i32, [vp, vp, vp, i32, i32, i32, C.POINTER(RouteChoice), vp, vp, vp, sz, vp]),
+    "moe_route_select": (i32, [vp, i32, i64, vp, i32, i32, C.POINTER(RouteChoice), vp, vp, vp]),
+    "moe_fp4_linear": (i32, [C.POINTER(Fp4WeightDesc), vp, i32, i64, i32, vp, i64, vp, i32, i64, vp, vp]),
+    "moe_fp4_swiglu": (i32, [C.POINTER(Fp4WeightDesc), C.POINTER(Fp4WeightDesc), vp, i32, i64, i32, vp, i64,
+                             vp, vp]),
     "moe_slot_lookup": (i32, [vp, i32, vp, i32, i32, vp, C.POINTER(LookupResult), vp]),
     "moe_slot_lookup_launch": (i32, [vp, i32, vp, i32, i32, vp, vp]),
     "moe_slot_lookup_result": (i32, [vp, C.POINTER(LookupResult)]),

@@ -7,6 +7,7 @@ the MoE layer runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import numpy as np
 import torch
@@ -128,6 +129,142 @@ def route_noalloc(x, wr, bias, k, renormalize, idx, w, stream=None):
     E = wr.shape[0]
     L.check("moe_route_noalloc", L.load().moe_route_noalloc(
         _p(x), _p(wr), _p(bias), T, H, E, int(k), int(renormalize), _p(idx), _p(w), _s(stream)))
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, dtypes, shape, what):
+    """Checks a 2-D tensor with contiguous rows; returns its row stride in elements."""
+    _need(t.dtype in dtypes and tuple(t.shape) == shape, f"{what} must be {shape} of {' or '.join(map(str, dtypes))}")
+    _need(t.stride(1) == 1 or shape[1] == 1, f"{what} must have contiguous rows")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _call(name, tensors, stream, *args):
+    """Library call on the device that holds all of `tensors`, on `stream` or that
+    device's current stream."""
+    dev = tensors[0].device
+    _need(dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
+          f"{name}: all tensors must be on one CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    _need(stream.device == dev, f"{name}: the stream belongs to another device than the tensors")
+    fn = getattr(L.load(), name)
+    if torch.cuda.current_device() == dev.index:
+        L.check(name, fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            L.check(name, fn(*args, stream.cuda_stream))
+
+
+_SCORE = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
+_TYPE = {torch.bfloat16: L.MOE_BF16, torch.float32: L.MOE_F32}
+
+
+@functools.lru_cache(maxsize=64)
+def _choice(k, score, n_group, topk_group, group_top, renormalize, scale):
+    _need(score in _SCORE, f"score must be one of {sorted(_SCORE)}")
+    return L.RouteChoice(k, _SCORE[score], n_group, topk_group, group_top, int(renormalize), scale)
+
+
+def _choice_outputs(T, E, idx, w, bias):
+    k = idx.shape[-1]
+    _need(idx.dtype == torch.int32 and tuple(idx.shape) == (T, k) and idx.is_contiguous(),
+          "idx must be a contiguous int32 [T, k]")
+    _need(w.dtype == torch.float32 and tuple(w.shape) == (T, k) and w.is_contiguous(),
+          "w must be a contiguous float32 [T, k]")
+    _need(bias is None or (bias.dtype == torch.float32 and tuple(bias.shape) == (E,) and bias.is_contiguous()),
+          "bias must be a contiguous float32 [E]")
+    return k
+
+
+def route_grouped_workspace_bytes(T, E):
+    return L.load().moe_route_grouped_workspace_bytes(int(T), int(E))
+
+
+def route_grouped(x, wr, idx, w, workspace, *, score="sigmoid", bias=None, n_group=1, topk_group=1, group_top=1,
+                  renormalize=True, scale=1.0, stream=None):
+    """moe_route_grouped: x [T, H] and wr [E, H] bf16 -> idx [T, k] int32 and w [T, k]
+    fp32.  Experts are chosen by sigmoid or softmax score + bias [E] fp32 (which does
+    not enter the weights; -inf masks an expert) within the topk_group best of n_group
+    groups, a group counting its group_top (1 or 2) best; w = scale * score, over the
+    chosen scores' sum if renormalize.  workspace: route_grouped_workspace_bytes(T, E)
+    bytes, zeroed before its first use."""
+    _need(x.dim() == 2 and wr.dim() == 2 and x.dtype == wr.dtype == torch.bfloat16 and x.shape[1] == wr.shape[1]
+          and x.is_contiguous() and wr.is_contiguous(), "x [T, H] and wr [E, H] must be contiguous bfloat16")
+    T, H = x.shape
+    E = wr.shape[0]
+    k = _choice_outputs(T, E, idx, w, bias)
+    _need(workspace.is_contiguous(), "the workspace must be contiguous")
+    _call("moe_route_grouped", (x, wr, idx, w, workspace, bias), stream, x.data_ptr(), wr.data_ptr(),
+          None if bias is None else bias.data_ptr(), T, H, E,
+          C.byref(_choice(k, score, n_group, topk_group, group_top, bool(renormalize), float(scale))), idx.data_ptr(),
+          w.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def route_select(logits, idx, w, *, score="sigmoid", bias=None, n_group=1, topk_group=1, group_top=1,
+                 renormalize=True, scale=1.0, stream=None):
+    """moe_route_select: route_grouped's choice on given logits [T, E], bf16 or fp32
+    with any row stride (a logit of -inf masks its expert)."""
+    _need(logits.dim() == 2, "logits must be [T, E]")
+    T, E = logits.shape
+    ld = _rows(logits, tuple(_TYPE), (T, E), "logits")
+    k = _choice_outputs(T, E, idx, w, bias)
+    _call("moe_route_select", (logits, idx, w, bias), stream, logits.data_ptr(), _TYPE[logits.dtype], ld,
+          None if bias is None else bias.data_ptr(), T, E,
+          C.byref(_choice(k, score, n_group, topk_group, group_top, bool(renormalize), float(scale))), idx.data_ptr(),
+          w.data_ptr())
+
+
+def _status(t):
+    _need(t.dtype == torch.int32 and t.numel() >= 1, "status must be an int32 tensor")
+    return t.data_ptr()
+
+
+class FP4Weight:
+    """A 4-bit matrix [N, K] on the device (moe_fp4_weight): codes [N, K/2] uint8 (the
+    lower index in the low nibble), block scales [N, K/32] (mxfp4, E8M0) or [N, K/16]
+    (nvfp4, E4M3) uint8, and NVFP4's tensor scale.  Keeps the tensors."""
+
+    def __init__(self, codes, scales, fmt, tensor_scale=1.0):
+        _need(fmt in FMT, f"fmt must be one of {sorted(FMT)}")
+        _need(codes.dim() == 2 and scales.dim() == 2 and codes.dtype == scales.dtype == torch.uint8
+              and codes.is_contiguous() and scales.is_contiguous(), "codes and scales must be contiguous 2-D uint8")
+        N, K = codes.shape[0], codes.shape[1] * 2
+        _need(K % 32 == 0 and K > 0 and N > 0, "K must be a positive multiple of 32, N positive")
+        _need(tuple(scales.shape) == (N, K // (32 if fmt == "mxfp4" else 16)),
+              "scales must be [N, K/32] (mxfp4) or [N, K/16] (nvfp4)")
+        _need(codes.device.type == "cuda" and codes.device == scales.device,
+              "codes and scales must be on one CUDA device")
+        self.codes, self.scales, self.fmt, self.tensor_scale = codes, scales, fmt, float(tensor_scale)
+        self.N, self.K = N, K
+        self._desc = L.Fp4WeightDesc(codes.data_ptr(), scales.data_ptr(), self.tensor_scale, N, K, FMT[fmt])
+        self.ref = C.byref(self._desc)
+
+
+def fp4_linear(x, weight, y, status, add=None, stream=None):
+    """moe_fp4_linear: y [T, N] (bf16 or fp32) = add + x W^T for x [T, K] (bf16 or fp32),
+    T <= 16.  add: None or like y (it may be y itself).  Row strides are free."""
+    _need(x.dim() == 2, "x must be [T, K]")
+    T = x.shape[0]
+    ldx = _rows(x, tuple(_TYPE), (T, weight.K), "x")
+    ldy = _rows(y, tuple(_TYPE), (T, weight.N), "y")
+    lda = 0 if add is None else _rows(add, (y.dtype,), (T, weight.N), "add")
+    _call("moe_fp4_linear", (x, weight.codes, y, status, add), stream, weight.ref, x.data_ptr(), _TYPE[x.dtype], ldx,
+          T, None if add is None else add.data_ptr(), lda, y.data_ptr(), _TYPE[y.dtype], ldy, _status(status))
+
+
+def fp4_swiglu(x, gate, up, h, status, stream=None):
+    """moe_fp4_swiglu: h [T, N] fp32 = silu(x W_gate^T) * (x W_up^T), T <= 16."""
+    _need(x.dim() == 2, "x must be [T, K]")
+    T = x.shape[0]
+    ldx = _rows(x, tuple(_TYPE), (T, gate.K), "x")
+    ldh = _rows(h, (torch.float32,), (T, gate.N), "h")
+    _call("moe_fp4_swiglu", (x, gate.codes, up.codes, h, status), stream, gate.ref, up.ref, x.data_ptr(),
+          _TYPE[x.dtype], ldx, T, h.data_ptr(), ldh, _status(status))
 
 
 class Lookup:

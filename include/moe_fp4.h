@@ -87,6 +87,33 @@ typedef struct {
 
 typedef struct moe_pool moe_pool;
 
+/* Element types of activations where a call takes more than bf16. */
+enum { MOE_BF16 = 0, MOE_F32 = 1 };
+
+/* Scores of the grouped router. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* How the grouped router chooses (moe_route_grouped, moe_route_select). */
+typedef struct {
+    int k;            /* experts chosen per token, <= 32 */
+    int score;        /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+    int n_group;      /* groups of E / n_group neighbouring experts, <= 32 (1: no groups) */
+    int topk_group;   /* groups a token may use */
+    int group_top;    /* a group's value: the sum of its 1 or 2 largest selection values */
+    int renormalize;  /* 1: divide the chosen scores by their sum */
+    float scale;      /* factor of every weight, positive and finite */
+} moe_route_choice;
+
+/* One 4-bit matrix in the canonical layout (device memory): y = W x has N outputs
+ * and K inputs.  The caller keeps the buffers. */
+typedef struct {
+    const uint8_t* codes;    /* [N, K/2], 16-byte aligned */
+    const uint8_t* scales;   /* [N, K/bs] block scales; NVFP4 scales are not negative */
+    float tensor_scale;      /* NVFP4 only (ignored for MXFP4) */
+    int N, K;                /* K a multiple of 32, any N */
+    int fmt;                 /* MOE_MXFP4 or MOE_NVFP4 */
+} moe_fp4_weight;
+
 /* One expert in the canonical layout (host memory).  tensor_scale[i] is the
  * NVFP4 FP32 tensor scale of gate/up/down (ignored for MXFP4). */
 typedef struct {
@@ -203,6 +230,58 @@ int moe_route(const void* x_bf16, const void* wr_bf16, const float* bias, int T,
  * until the process exits.  Allocates nothing (no cudaMalloc / cudaFree). */
 int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H,
                       int E, int k, int renormalize, int32_t* idx, float* w, void* stream);
+
+/* Grouped router, for models that score with a sigmoid or with the full softmax,
+ * steer the choice with a balance bias and limit a token to a few groups of
+ * experts (no counterpart on the pages, whose gate is moe_route).  Per token, with
+ * l = x W_r^T:
+ *   s_e = 1 / (1 + exp(-l_e))  or  softmax(l)_e          the score
+ *   c_e = s_e + bias_e                                   the selection value
+ *   the topk_group groups with the largest sums of their group_top largest c, then
+ *   the k experts with the largest c in those groups; equal values go to the lower
+ *   group or expert index; ranks in descending c
+ *   w_j = scale * s_j, divided by the sum of the chosen s if renormalize
+ * bias may be NULL; it never enters the weights.  The choice is made on 64-bit
+ * values of the exact logits, so it does not depend on T or on the order of sums.
+ * bias_e = -inf masks expert e: it adds nothing to its group's value, ranks below
+ * every unmasked expert of the kept groups (then by index) and has weight 0.  A NaN
+ * selection value ranks like a masked one and its weight is NaN.  Where the chosen
+ * scores sum to 0 the renormalised weights are 0.  idx is always within [0, E).
+ * x [T, H] and W_r [E, H] bf16, 16-byte aligned rows (H % 8 == 0); outputs idx
+ * [T, k] int32 and w [T, k] fp32 in rank order.  workspace: device scratch of
+ * moe_route_grouped_workspace_bytes(T, E) bytes, 16-byte aligned, zeroed before its
+ * first use (every call leaves its counters zero); calls that may overlap, and
+ * captured graphs that may be replayed at the same time, need one each.  E <= 1024.
+ * Errors: MOE_EINVAL. */
+size_t moe_route_grouped_workspace_bytes(int T, int E);
+int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H, int E,
+                      const moe_route_choice* choice, int32_t* idx, float* w, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The choice of moe_route_grouped on logits the caller has: [T, E] of `type`
+ * (MOE_BF16 or MOE_F32) with a row stride of ld elements.  A logit of -inf masks
+ * its expert like a bias of -inf, and a softmax over nothing else gives score 0.
+ * No workspace.  Errors: MOE_EINVAL. */
+int moe_route_select(const void* logits, int type, long long ld, const float* bias, int T, int E,
+                     const moe_route_choice* choice, int32_t* idx, float* w, void* stream);
+
+/* Product of a few tokens with a 4-bit matrix, for the dense parts beside the routed
+ * experts (a shared expert, projections, an output head) in the experts' formats:
+ *   y[t, n] = add[t, n] + S * sum_k x[t, k] * e2m1(codes[n, k]) * scale[n, k / bs]
+ * x [T, K] of x_type (rows 16-byte aligned), y [T, N] of y_type, add NULL or [T, N]
+ * of y_type (it may be y itself: y += W x; otherwise no output may overlap an
+ * input); row strides ldx, ld_add, ldy in elements.  Sums in fp32, one rounding to
+ * y_type at the end.  T from 1 to 16.  Bounded device waits set bit 16 of *status
+ * (device int, caller-zeroed) on timeout.  Errors: MOE_EINVAL. */
+int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type, long long ldx, int T, const void* add,
+                   long long ld_add, void* y, int y_type, long long ldy, int* status, void* stream);
+
+/* The gated pair of a SwiGLU expert: h[t, i] = silu(g) * u, g = W_gate x, u = W_up x,
+ * for two 4-bit matrices of one shape and format; h [T, N] fp32 with row stride ldh,
+ * so that moe_fp4_linear can take it as x without a rounding between.  Rules and
+ * errors as moe_fp4_linear. */
+int moe_fp4_swiglu(const moe_fp4_weight* gate, const moe_fp4_weight* up, const void* x, int x_type, long long ldx,
+                   int T, float* h, long long ldh, int* status, void* stream);
 
 /* LRU slot lookup (post.smzdm.com/p/aomxznrn, "FreeToken干的事": a global LRU
  * expert-slot pool).  One kernel, one CTA: the unique experts of idx in
