@@ -1,86 +1,500 @@
 // Products of a few tokens with one 4-bit matrix: y = add + W x, and the gated
-// pair h = silu(W_gate x) * (W_up x).
+// pair h = silu(W_gate x) * (W_up x), on the block-scaled FP4 tensor cores.
 //
-// One warp per output row; lane j takes the 32-element chunks c with c % 32 == j
-// (16 code bytes), dequantises them and sums its products in fp32.
-#include "common.cuh"
+// The tensor core multiplies E2M1 by E2M1 and applies W's block scales itself, so
+// the weights go from HBM to shared memory to the MMA untouched, with no
+// dequantisation on the way (on the CUDA cores that costs 2-3 instructions a weight
+// and keeps them from reading at HBM speed).  What has to become E2M1 is x, and it
+// does so without loss: with E the exponent of a token's largest |x| in the CTA's
+// share of K, X = rint(x 2^(21 - E)) is a 23-bit integer, and
+//     X = sum_d u_d 8^d,  u_d in {-4 .. 3},  d = 0 .. 7
+// in balanced octal digits, each of them an E2M1 value.  The 8 digits of a token are
+// 8 columns of the MMA's B operand, D_d = W u_d is exact up to fp32 accumulation,
+// and  W x = 2^E sum_d 8^(d - 7) D_d.  (bf16 elements down to 2^-14 of the largest
+// enter exactly, smaller ones and fp32 elements to 2^-22 of the largest.)  Sixteen
+// tokens fill an N = 128 MMA, which still takes a third of the time HBM needs to
+// bring its 128 x 64 weights.
+//
+// A cluster of C CTAs shares the 128 rows of a tile, CTA r taking the r-th part Kc
+// of K: with few tiles this spreads a matrix over the SMs, and it keeps the digits
+// of a CTA's part of x (4 Kc bytes a token) resident in shared memory for all the
+// tiles the cluster works through.  The parts' sums meet in shared memory, row r of
+// a tile at the CTA that owns it, and are added in rank order, so the result does
+// not depend on timing.  Warp roles:
+//   warp 0       TMA producer: a 128-row x 256-element code tile per stage
+//   warp 1       MMA issuer (owns the TMEM allocation)
+//   warps 1-7    digits of x, first
+//   warps 4-7    epilogue: TMEM -> digit sum -> exchange over the cluster -> y
+//   warps 8-11   one row each: block scales from global memory into the tensor
+//                core's scale-factor layout (see gemm_fp4.cu)
+// The gated form puts 64 gate rows and the same 64 up rows in one tile.
+// All waits are bounded; a timeout sets bit 16 of *status and the CTA carries on.
+#include "tcgen05.cuh"
 
 namespace moe {
 
-constexpr int kLinWarps = 8;
+int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
+                 uint32_t box_bytes, uint32_t box_rows, bool swizzle128);
 
-struct Fp4Mat {
-    const uint8_t* codes;
+constexpr int kLinThreads = 384;
+constexpr int kLinKT = 256;               // K elements of a stage (128 code bytes a row)
+constexpr int kLinMaxStages = 8;
+constexpr int kLinMaxCluster = 8;
+constexpr int kLinPrepWarps = 7;          // warps 1 .. 7
+
+struct LinMat {
     const uint8_t* scales;
     float ts;
 };
 struct LinArgs {
-    Fp4Mat m[2];
-    int N, K, T, x_f32, y_f32;
+    LinMat m[2];
+    int N, K, T;
+    int Kc;              // K elements per CTA, a multiple of kLinKT
+    int C;               // CTAs per cluster
+    int stages;
+    int tiles;
+    int wide_scales;     // scale rows can be read 16 (NVFP4) or 8 (MXFP4) bytes at a time
+    uint32_t tmem_cols;
+    int x_f32, y_f32;
     const void* x;
     long long ldx;
     const void* add;
     long long ld_add;
     void* y;
     long long ldy;
+    int* status;
+    unsigned long long limit_ns;
 };
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-    return (c & 8u) ? -v : v;
-}
-__device__ __forceinline__ float e4m3_value(uint32_t b) {
-    const uint32_t ex = (b >> 3) & 15u, mn = b & 7u;
-    float v = ex ? __uint_as_float(((ex + 120u) << 23) | (mn << 20)) : (float)mn * 0.001953125f;
-    if ((b & 0x7fu) == 0x7fu) v = __uint_as_float(0x7fc00000u);
-    return (b & 0x80u) ? -v : v;
-}
-__device__ __forceinline__ float e8m0_value(uint32_t b) {
-    return b == 255u ? __uint_as_float(0x7fc00000u) : b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u);
-}
-__device__ __forceinline__ float load_act(const void* p, int f32, long long i) {
-    return f32 ? static_cast<const float*>(p)[i]
-               : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+// Shared-memory offsets from the 1024-aligned base.
+struct LinSmem {
+    int codes, atoms, digits, ones, exch, bars, total;
+    __host__ __device__ LinSmem(int stages, int Tp, int Kc, int C, int T, int gated) {
+        codes = 0;
+        digits = codes + stages * 16384;
+        atoms = digits + Tp * 8 * (Kc / 2);
+        ones = atoms + stages * 2048;
+        exch = ones + 512;
+        const int out = gated ? 64 : 128, R = (out + C - 1) / C;
+        bars = exch + 2 * 4 * C * (gated ? 2 : 1) * T * R;
+        bars = (bars + 15) / 16 * 16;
+        total = bars + (3 * kLinMaxStages + 7) * 8 + 2 * 16 * 4 + 2 * 16 * 4 + 32;
+    }
+};
+
+// D[tmem] (+)= A[smem] x B[smem]^T with 32-element E8M0 block scales from TMEM.
+__device__ __forceinline__ void mma_mxfp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p; }"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
 }
 
-template <int FMT, int GATED>
-__global__ void __launch_bounds__(kLinWarps * 32) fp4_linear_kernel(const LinArgs a) {
-    const int lane = threadIdx.x & 31, n = blockIdx.x * kLinWarps + (threadIdx.x >> 5);
-    pdl_trigger();
-    pdl_wait();
-    if (n >= a.N) return;
-    constexpr int BS = FMT == MOE_MXFP4 ? 32 : 16;
-    for (int t = 0; t < a.T; t++) {
-        float acc[2] = {0.0f, 0.0f};
-        for (int c = lane; c < a.K / 32; c += 32)
-            for (int m = 0; m <= GATED; m++) {
-                const uint8_t* cp = a.m[m].codes + (size_t)n * (a.K / 2) + c * 16;
-                const uint8_t* sp = a.m[m].scales + (size_t)n * (a.K / BS) + c * (32 / BS);
-                for (int b = 0; b < 32 / BS; b++) {
-                    float part = 0.0f;
-                    for (int i = 0; i < BS / 2; i++) {
-                        const uint32_t v = cp[b * (BS / 2) + i];
-                        const long long k = c * 32 + b * BS + 2 * i;
-                        part = fmaf(e2m1_value(v & 15u), load_act(a.x, a.x_f32, t * a.ldx + k), part);
-                        part = fmaf(e2m1_value(v >> 4), load_act(a.x, a.x_f32, t * a.ldx + k + 1), part);
-                    }
-                    acc[m] = fmaf(part, FMT == MOE_MXFP4 ? e8m0_value(sp[b]) : e4m3_value(sp[b]), acc[m]);
-                }
-            }
-        for (int off = 16; off >= 1; off >>= 1)
-            for (int m = 0; m <= GATED; m++) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], off);
-        if (lane) continue;
-        float v = acc[0] * a.m[0].ts;
-        if (GATED) {
-            const float u = acc[1] * a.m[1].ts;
-            v = v / (1.0f + expf(-v)) * u;
-        }
-        if (a.add) v += load_act(a.add, a.y_f32, t * a.ld_add + n);
-        if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
-        else static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + n] = __float2bfloat16_rn(v);
+// 32 lanes x 8 consecutive fp32 columns; complete after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;"
+            " selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if (globaltimer() - t0 > limit_ns) return false;
     }
 }
+
+// Bring a tile of global memory towards L2 only: no thread sees the data, so it may
+// run before the kernel's wait for its predecessor.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
+// ---------------------------------------------------------------- x digits
+
+// 8 consecutive elements of row t from k (k % 8 == 0); zeros from K on.
+__device__ __forceinline__ void load_x8(const LinArgs& a, int t, int k, float (&v)[8]) {
+    if (t >= a.T || k >= a.K) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = 0.0f;
+    } else if (a.x_f32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + t * a.ldx + k);
+        const float4 p0 = p[0], p1 = p[1];
+        v[0] = p0.x; v[1] = p0.y; v[2] = p0.z; v[3] = p0.w;
+        v[4] = p1.x; v[5] = p1.y; v[6] = p1.z; v[7] = p1.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.ldx + k);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// X (|X| <= 2^22) as 8 selector nibbles u_d + 4, the lowest digit in the lowest nibble.
+__device__ __forceinline__ uint32_t octal_nibbles(int X) {
+    const uint32_t u = (uint32_t)(X + 0x924924);          // 4 (8^8 - 1) / 7
+    const uint32_t w = (u & 0xFFFu) | ((u & 0xFFF000u) << 4);
+    return (w & 0x00070007u) | ((w & 0x00380038u) << 1) | ((w & 0x01C001C0u) << 2) | ((w & 0x0E000E00u) << 3);
+}
+
+// 8 elements -> for each digit d the 4 bytes (8 codes) of B's row d.
+__device__ __forceinline__ void digit_rows(const int (&X)[8], uint32_t (&row)[8]) {
+    // E2M1 codes of -4 -3 -2 -1 | 0 1 2 3, and the same in the high nibble
+    constexpr uint32_t la = 0x0A0C0D0Eu, lb = 0x05040200u, ha = la << 4, hb = lb << 4;
+    uint32_t p[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t s0 = octal_nibbles(X[2 * i]), s1 = octal_nibbles(X[2 * i + 1]);
+        p[0][i] = __byte_perm(la, lb, s0) | __byte_perm(ha, hb, s1);
+        p[1][i] = __byte_perm(la, lb, s0 >> 16) | __byte_perm(ha, hb, s1 >> 16);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {   // 4 x 4 byte transpose
+        const uint32_t t0 = __byte_perm(p[h][0], p[h][1], 0x5140), t1 = __byte_perm(p[h][2], p[h][3], 0x5140);
+        const uint32_t t2 = __byte_perm(p[h][0], p[h][1], 0x7362), t3 = __byte_perm(p[h][2], p[h][3], 0x7362);
+        row[4 * h + 0] = __byte_perm(t0, t1, 0x5410);
+        row[4 * h + 1] = __byte_perm(t0, t1, 0x7632);
+        row[4 * h + 2] = __byte_perm(t2, t3, 0x5410);
+        row[4 * h + 3] = __byte_perm(t2, t3, 0x7632);
+    }
+}
+
+// ---------------------------------------------------------------- block scales
+
+// The scales of one row and stage as 4 words, one per 64 elements: NVFP4 its 4
+// bytes, MXFP4 its 2 in the low half.  p: the stage's first scale of the row, n:
+// how many scales the row has from there (0 for a row or stage outside).
+template <int FMT>
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide) {
+    constexpr int per = FMT == MOE_NVFP4 ? 16 : 8;   // scales per stage
+    uint32_t b[4] = {0, 0, 0, 0};
+    if (n >= per && wide) {
+        if constexpr (FMT == MOE_NVFP4) return __ldg(reinterpret_cast<const uint4*>(p));
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        b[0] = v.x;
+        b[1] = v.y;
+    } else if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < per; i++)
+            if (i < n) b[i / 4] |= (uint32_t)__ldg(p + i) << (8 * (i % 4));
+    }
+    if constexpr (FMT == MOE_NVFP4) return make_uint4(b[0], b[1], b[2], b[3]);
+    return make_uint4(b[0] & 0xFFFFu, b[0] >> 16, b[1] & 0xFFFFu, b[1] >> 16);
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int FMT, int GATED>
+__global__ void __launch_bounds__(kLinThreads, 1)
+fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+                  const LinArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = a.stages, C = a.C, T = a.T, Tp = (T + 1) & ~1;
+    const LinSmem L(S, Tp, a.Kc, C, T, GATED);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars);      // codes landed
+    uint64_t* sfull = full + kLinMaxStages;                         // scales written
+    uint64_t* empty = sfull + kLinMaxStages;                        // stage read by its MMAs
+    uint64_t* accf = empty + kLinMaxStages;                         // [2] accumulator complete
+    uint64_t* acce = accf + 2;                                      // [2] accumulator read
+    uint64_t* exf = acce + 2;                                       // [2] exchange buffer complete
+    uint64_t* bready = exf + 2;                                     // digits of x complete
+    uint32_t* xmax = reinterpret_cast<uint32_t*>(bready + 1);       // [16] largest |x| bits, then 2 x [16] 2^E
+    float* xscale = reinterpret_cast<float*>(xmax + 16);
+    uint32_t* tmem_slot = xmax + 48;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
+    const int cl = blockIdx.x / C, ncl = gridDim.x / C;
+    const int k0 = rank * a.Kc;
+    const int steps = (min(a.K - k0, a.Kc) + 63) / 64;              // 64-element MMA steps of this CTA
+    const int KT = (steps + 3) / 4;                                 // stages per tile
+    constexpr int TR = GATED ? 64 : 128;                            // rows of each matrix per tile
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfull[s], 4);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&acce[i], 4);
+            mbar_init(&exf[i], 4 * C);
+        }
+        mbar_init(bready, kLinPrepWarps);
+        fence_mbar_init();
+        prefetch_tmap(&map0);
+        if (GATED) prefetch_tmap(&map1);
+    }
+    if (threadIdx.x < 16) xmax[threadIdx.x] = 0;
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + 128)
+        reinterpret_cast<uint32_t*>(sm + L.ones)[threadIdx.x - 64] = FMT == MOE_NVFP4 ? 0x38383838u : 0x7F7F7F7Fu;
+    if (warp == 1) tmem_alloc(tmem_slot, a.tmem_cols);
+    fence_proxy_async_smem();   // the scale atom of ones
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (C > 1) cluster_arrive();   // peers may write here once every CTA's barriers are set
+    const uint32_t tbase = *tmem_slot;
+    const uint32_t sf_base = tbase + 2 * 8 * Tp, sfb = sf_base + 16 * S;
+    pdl_trigger();
+    if (warp == 0 && lane == 0) {
+        // the first stages' codes, while the kernel before this one finishes
+        int n = 0;
+        for (int tile = cl; tile < a.tiles && n < S; tile += ncl)
+            for (int kt = 0; kt < KT && n < S; kt++, n++) {
+                tma_prefetch_2d(&map0, k0 / 2 + kt * 128, tile * TR);
+                if (GATED) tma_prefetch_2d(&map1, k0 / 2 + kt * 128, tile * TR);
+            }
+    } else if (warp >= 8) {
+        const int r = threadIdx.x - 256, which = GATED ? r >> 6 : 0, n = cl * TR + (GATED ? r & 63 : r);
+        constexpr int BS = FMT == MOE_NVFP4 ? 16 : 32;
+        if (n < a.N)
+            for (int o = 0; o < min(a.K - k0, a.Kc) / BS; o += 128)
+                prefetch_l2(a.m[which].scales + (size_t)n * (a.K / BS) + k0 / BS + o);
+    }
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int tile = cl; tile < a.tiles; tile += ncl)
+                for (int kt = 0; kt < KT; kt++, it++) {
+                    const int s = it % S, r = it / S;
+                    if (!mbar_wait(&empty[s], (r & 1) ^ 1, a.limit_ns)) atomicOr(a.status, 1 << 16);
+                    mbar_arrive_expect_tx(&full[s], 16384);
+                    uint8_t* dst = sm + L.codes + s * 16384;
+                    const int c0 = k0 / 2 + kt * 128;
+                    tma_load_2d(dst, &map0, c0, tile * TR, &full[s]);
+                    if (GATED) tma_load_2d(dst + 8192, &map1, c0, tile * TR, &full[s]);
+                }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        const int r = threadIdx.x - 256, which = GATED ? r >> 6 : 0, rr = GATED ? r & 63 : r;
+        constexpr int BS = FMT == MOE_NVFP4 ? 16 : 32, per = kLinKT / BS;
+        const int pitch = a.K / BS;
+        const uint8_t* base = a.m[which].scales + k0 / BS;
+        const int have = min(a.K - k0, a.Kc) / BS;       // scales of this CTA's part of a row
+        const int total = cl < a.tiles ? ((a.tiles - cl + ncl - 1) / ncl) * KT : 0;
+        auto fetch = [&](int it) -> uint4 {
+            const int n = (cl + (it / KT) * ncl) * TR + rr, o = (it % KT) * per;
+            const bool in = it < total && n < a.N;
+            return load_scales<FMT>(base + (in ? (size_t)n * pitch + o : 0), in ? have - o : 0, a.wide_scales);
+        };
+        uint4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) q[i] = fetch(i);
+        for (int it0 = 0; it0 < total; it0 += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int it = it0 + i;
+                if (it < total) {
+                    const int s = it % S;
+                    if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                    uint8_t* atom = sm + L.atoms + s * 2048 + 16 * (r & 31) + 4 * (r >> 5);
+                    *reinterpret_cast<uint32_t*>(atom) = q[i].x;
+                    *reinterpret_cast<uint32_t*>(atom + 512) = q[i].y;
+                    *reinterpret_cast<uint32_t*>(atom + 1024) = q[i].z;
+                    *reinterpret_cast<uint32_t*>(atom + 1536) = q[i].w;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfull[s]);
+                }
+                q[i] = fetch(it + 4);
+            }
+        }
+    } else {
+        // digits of x: items are (token, 256 elements), 8 elements per lane
+        const int pw = warp - 1, items = Tp * KT;
+        for (int j = pw; j < items; j += kLinPrepWarps) {
+            float v[8];
+            load_x8(a, j / KT, k0 + (j % KT) * kLinKT + lane * 8, v);
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) mx = max(mx, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            if (lane == 0) atomicMax(&xmax[j / KT], mx);
+        }
+        named_sync(1, kLinPrepWarps * 32);
+        for (int j = pw; j < items; j += kLinPrepWarps) {
+            const int t = j / KT, kt = j % KT;
+            const uint32_t mx = xmax[t];
+            // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
+            const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
+            const bool finite = mx < 0x7F800000u;
+            const int up = 21 - E, h1 = up / 2, d1 = E / 2;
+            const float f1 = exp2i(h1), f2 = exp2i(up - h1);
+            float v[8];
+            load_x8(a, t, k0 + kt * kLinKT + lane * 8, v);
+            int X[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) X[i] = finite ? __float2int_rn(v[i] * f1 * f2) : 0;
+            uint32_t row[8];
+            digit_rows(X, row);
+            // rows 8 t + d of the K-major operand, 128-byte swizzle: 16-byte chunk c of row d at c ^ d
+            uint8_t* dst = sm + L.digits + (kt * Tp + t) * 1024;
+#pragma unroll
+            for (int d = 0; d < 8; d++)
+                *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = row[d];
+            if (kt == 0 && lane == 0) {
+                xscale[t] = finite ? exp2i(d1) : __uint_as_float(0x7FC00000u);
+                xscale[16 + t] = exp2i(E - d1);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bready);
+
+        if (warp == 1) {
+            if (lane == 0) {
+                if (!mbar_wait(bready, 0, a.limit_ns)) atomicOr(a.status, 1 << 16);
+                tc_fence_after();
+                const uint32_t idesc = idesc_fp4(128, 8 * Tp, FMT == MOE_MXFP4);
+                tmem_cp_sf_atom(sfb, smem_desc(sm + L.ones, 16, 128, 0));
+                int it = 0, tc = 0;
+                for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
+                    const int b = tc & 1;
+                    if (!mbar_wait(&acce[b], ((tc >> 1) & 1) ^ 1, a.limit_ns)) atomicOr(a.status, 1 << 16);
+                    tc_fence_after();
+                    const uint32_t acc = tbase + b * 8 * Tp;
+                    for (int kt = 0; kt < KT; kt++, it++) {
+                        const int s = it % S, r = it / S;
+                        if (!mbar_wait(&full[s], r & 1, a.limit_ns) || !mbar_wait(&sfull[s], r & 1, a.limit_ns))
+                            atomicOr(a.status, 1 << 16);
+                        tc_fence_after();
+                        const uint32_t sfa = sf_base + 16 * s;
+                        const int ns = min(4, steps - 4 * kt);
+                        for (int i = 0; i < ns; i++)
+                            tmem_cp_sf_atom(sfa + 4 * i, smem_desc(sm + L.atoms + s * 2048 + 512 * i, 16, 128, 0));
+                        const uint64_t ad = smem_desc(sm + L.codes + s * 16384, 16, 1024, 2);
+                        const uint64_t bd = smem_desc(sm + L.digits + kt * Tp * 1024, 16, 1024, 2);
+                        for (int i = 0; i < ns; i++) {
+                            const uint32_t accum = (kt > 0 || i > 0) ? 1u : 0u;
+                            if (FMT == MOE_NVFP4) mma_nvfp4(acc, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sfb, accum);
+                            else mma_mxfp4(acc, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sfb, accum);
+                        }
+                        tc_commit(&empty[s]);
+                    }
+                    tc_commit(&accf[b]);
+                }
+            }
+            __syncwarp();
+        } else if (warp >= 4) {
+            if (!mbar_wait(bready, 0, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);   // xscale
+            const int e4 = warp - 4, row = 32 * e4 + lane;
+            const int R = (TR + C - 1) / C;                   // output rows per owner
+            const int orow = GATED ? row & 63 : row, which = GATED ? row >> 6 : 0;
+            const int owner = orow / R;
+            constexpr int NW = GATED ? 2 : 1;
+            const int buf_words = C * NW * T * R;
+            const float ts = a.m[which].ts;
+            float* exch = reinterpret_cast<float*>(sm + L.exch);
+            // where this row's values go: [src][which][t][row - owner * R] of the owner's buffer
+            const uint32_t dst = (C > 1 ? map_rank(smem_addr(exch), owner) : smem_addr(exch)) +
+                                 4 * ((rank * NW + which) * T * R + orow - owner * R);
+            const int own0 = rank * R, nown = max(0, min(R, TR - own0));
+            if (C > 1) cluster_wait();                        // peers' barriers are set
+            int tc = 0;
+            for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
+                const int b = tc & 1;
+                if (!mbar_wait(&accf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                tc_fence_after();
+                const uint32_t acc = tbase + b * 8 * Tp + ((uint32_t)(32 * e4) << 16);
+                for (int t0 = 0; t0 < T; t0 += 2) {
+                    uint32_t d[2][8];
+                    tmem_ld_32x8(acc + 8 * t0, d[0]);
+                    tmem_ld_32x8(acc + 8 * t0 + 8, d[1]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int t = t0 + h;
+                        if (t >= T) break;
+                        float v = __uint_as_float(d[h][0]);
+#pragma unroll
+                        for (int q = 1; q < 8; q++) v = fmaf(v, 0.125f, __uint_as_float(d[h][q]));
+                        v = v * ts * xscale[t] * xscale[16 + t];
+                        st_cluster_f32(dst + 4 * (b * buf_words + t * R), v);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acce[b]);
+                if (lane < C) mbar_arrive_cluster(C > 1 ? map_rank(smem_addr(&exf[b]), lane) : smem_addr(&exf[b]));
+                if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                const float* in = exch + b * buf_words;
+                for (int j = threadIdx.x - 128; j < T * R; j += 128) {
+                    const int t = j / R, o = j - t * R, n = tile * TR + own0 + o;
+                    if (o >= nown || n >= a.N) continue;
+                    float v = 0.0f, u = 0.0f;
+                    for (int c = 0; c < C; c++) {
+                        v += in[c * NW * T * R + j];
+                        if (GATED) u += in[(c * NW + 1) * T * R + j];
+                    }
+                    if (GATED) v = v / (1.0f + expf(-v)) * u;
+                    if (a.add)
+                        v += a.y_f32 ? static_cast<const float*>(a.add)[t * a.ld_add + n]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.add)[t * a.ld_add + n]);
+                    if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
+                    else static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + n] = __float2bfloat16_rn(v);
+                }
+            }
+        }
+    }
+    // the cluster's CTAs leave together: none may end while a peer still writes to it
+    if (C > 1) {
+        __syncwarp();
+        if (warp < 4 || warp >= 8) cluster_wait();   // the epilogue warps waited above
+        cluster_arrive();
+        cluster_wait();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, a.tmem_cols);
+    }
+}
+
+// ---------------------------------------------------------------- host
 
 static int check_weight(const moe_fp4_weight* w) {
     if (!w || !w->codes || !w->scales) return fail(MOE_EINVAL, "fp4 weight: null pointer");
@@ -99,14 +513,124 @@ static int check_rows(const void* p, int type, long long ld, int width, int T, c
     return MOE_OK;
 }
 
-static int launch(const LinArgs& a, int fmt, int gated, cudaStream_t s) {
-    const dim3 grid((a.N + kLinWarps - 1) / kLinWarps), block(kLinWarps * 32);
-    cudaError_t e;
-    if (fmt == MOE_MXFP4) e = gated ? launch_pdl(fp4_linear_kernel<MOE_MXFP4, 1>, grid, block, 0, s, a)
-                                    : launch_pdl(fp4_linear_kernel<MOE_MXFP4, 0>, grid, block, 0, s, a);
-    else e = gated ? launch_pdl(fp4_linear_kernel<MOE_NVFP4, 1>, grid, block, 0, s, a)
-                   : launch_pdl(fp4_linear_kernel<MOE_NVFP4, 0>, grid, block, 0, s, a);
-    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "fp4 linear launch");
+struct LinDevice {
+    int sms = 0;
+    int smem = 0;                              // dynamic shared memory a block may take
+    int clusters[4][kLinMaxCluster + 1] = {};  // co-resident clusters per kernel and cluster size
+};
+
+template <int FMT, int GATED>
+static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& m1, LinDevice& d, cudaStream_t s) {
+    auto kern = fp4_linear_kernel<FMT, GATED>;
+    const int Tp = (a.T + 1) & ~1, KTall = (a.K + kLinKT - 1) / kLinKT;
+    a.tiles = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
+    int* active = d.clusters[FMT * 2 + GATED];
+    if (!active[1]) {
+        MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem));
+        for (int C = kLinMaxCluster; C >= 1; C--) {
+            cudaLaunchConfig_t lc = {};
+            lc.gridDim = dim3(C);
+            lc.blockDim = dim3(kLinThreads);
+            lc.dynamicSmemBytes = d.smem;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = C;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            lc.attrs = at;
+            lc.numAttrs = 1;
+            int n = 0;
+            MOE_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &lc));
+            active[C] = n < 1 ? 1 : n;
+        }
+    }
+    // Cluster size: the fewest stages on the busiest CTA, small clusters first.  The digits
+    // of x take 4 Tp Kc bytes; with at most 64 KiB of them 8 stages fit beside them.
+    int bestC = 0;
+    long long best = 0;
+    for (int cap = 64 * 1024; cap <= 128 * 1024 && !bestC; cap *= 2)
+        for (int C = 1; C <= kLinMaxCluster && C <= KTall; C++) {
+            const int kt = (KTall + C - 1) / C;
+            if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
+            if (4 * Tp * kt * kLinKT > cap) continue;
+            const int ncl = std::min(a.tiles, active[C]);
+            const long long cost = (long long)((a.tiles + ncl - 1) / ncl) * kt;
+            if (!bestC || cost < best) { best = cost; bestC = C; }
+        }
+    if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens (K * T, T rounded up to even, at most 262144)");
+    a.C = bestC;
+    const int kt = (KTall + a.C - 1) / a.C;
+    a.Kc = kt * kLinKT;
+    const int ncl = std::min(a.tiles, active[a.C]);
+    const long long total = (long long)((a.tiles + ncl - 1) / ncl) * kt;
+    a.stages = (int)std::min<long long>(kLinMaxStages, total);
+    while (a.stages > 1 && LinSmem(a.stages, Tp, a.Kc, a.C, a.T, GATED).total + 1024 > d.smem) a.stages--;
+    const int smem = LinSmem(a.stages, Tp, a.Kc, a.C, a.T, GATED).total + 1024;
+    if (smem > d.smem) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
+    const int cols = 2 * 8 * Tp + 16 * a.stages + 4;
+    a.tmem_cols = 32;
+    while ((int)a.tmem_cols < cols) a.tmem_cols *= 2;
+
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(ncl * a.C);
+    lc.blockDim = dim3(kLinThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.C;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = a.C > 1 ? 2 : 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&lc, kern, m0, m1, (const LinArgs)a));
+    return MOE_OK;
+}
+
+static LinDevice* lin_device(int& rc) {
+    static LinDevice devs[64];
+    int dev = -1;
+    rc = MOE_OK;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) { rc = cuda_fail(e, "cudaGetDevice"); return nullptr; }
+    if (dev < 0 || dev >= 64) { rc = fail(MOE_EINVAL, "fp4: device ordinal out of range"); return nullptr; }
+    LinDevice& d = devs[dev];
+    if (!d.sms) {
+        int smem = 0, sms = 0;
+        if ((e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) {
+            rc = cuda_fail(e, "cudaDeviceGetAttribute");
+            return nullptr;
+        }
+        d.smem = smem;
+        d.sms = sms;
+    }
+    return &d;
+}
+
+static int launch_linear(LinArgs& a, const moe_fp4_weight* w0, const moe_fp4_weight* w1, cudaStream_t s) {
+    int rc;
+    LinDevice* d = lin_device(rc);
+    if (!d) return rc;
+    const int bs = w0->fmt == MOE_NVFP4 ? 16 : 32;
+    const moe_fp4_weight* w[2] = {w0, w1};
+    CUtensorMap maps[2];
+    a.N = w0->N;
+    a.K = w0->K;
+    a.limit_ns = 2000000000ull;
+    uintptr_t low = (uintptr_t)(a.K / bs);
+    for (int i = 0; i < (w1 ? 2 : 1); i++) {
+        a.m[i] = LinMat{w[i]->scales, w[i]->fmt == MOE_NVFP4 ? w[i]->tensor_scale : 1.0f};
+        low |= reinterpret_cast<uintptr_t>(w[i]->scales);
+        if ((rc = make_tmap_2d(&maps[i], w[i]->codes, a.K / 2, a.N, a.K / 2, 128, w1 ? 64 : 128, true))) return rc;
+    }
+    if (!w1) maps[1] = maps[0];
+    a.wide_scales = low % (w0->fmt == MOE_NVFP4 ? 16 : 8) == 0;
+    if (w0->fmt == MOE_NVFP4)
+        return w1 ? launch_variant<MOE_NVFP4, 1>(a, maps[0], maps[1], *d, s)
+                  : launch_variant<MOE_NVFP4, 0>(a, maps[0], maps[1], *d, s);
+    return w1 ? launch_variant<MOE_MXFP4, 1>(a, maps[0], maps[1], *d, s)
+              : launch_variant<MOE_MXFP4, 0>(a, maps[0], maps[1], *d, s);
 }
 
 }  // namespace moe
@@ -125,12 +649,12 @@ extern "C" int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type
     if ((reinterpret_cast<uintptr_t>(x) & 15) || (T > 1 && (ldx * (x_type == MOE_BF16 ? 2 : 4)) % 16))
         return fail(MOE_EINVAL, "fp4 linear: rows of x must be 16-byte aligned");
     LinArgs a{};
-    a.m[0] = Fp4Mat{w->codes, w->scales, w->fmt == MOE_NVFP4 ? w->tensor_scale : 1.0f};
-    a.N = w->N; a.K = w->K; a.T = T;
+    a.T = T;
     a.x = x; a.x_f32 = x_type == MOE_F32; a.ldx = ldx;
     a.add = add; a.ld_add = ld_add;
     a.y = y; a.y_f32 = y_type == MOE_F32; a.ldy = ldy;
-    return launch(a, w->fmt, 0, (cudaStream_t)stream);
+    a.status = status;
+    return launch_linear(a, w, nullptr, (cudaStream_t)stream);
 }
 
 extern "C" int moe_fp4_swiglu(const moe_fp4_weight* gate, const moe_fp4_weight* up, const void* x, int x_type,
@@ -146,11 +670,9 @@ extern "C" int moe_fp4_swiglu(const moe_fp4_weight* gate, const moe_fp4_weight* 
     if ((reinterpret_cast<uintptr_t>(x) & 15) || (T > 1 && (ldx * (x_type == MOE_BF16 ? 2 : 4)) % 16))
         return fail(MOE_EINVAL, "fp4 swiglu: rows of x must be 16-byte aligned");
     LinArgs a{};
-    const bool nv = gate->fmt == MOE_NVFP4;
-    a.m[0] = Fp4Mat{gate->codes, gate->scales, nv ? gate->tensor_scale : 1.0f};
-    a.m[1] = Fp4Mat{up->codes, up->scales, nv ? up->tensor_scale : 1.0f};
-    a.N = gate->N; a.K = gate->K; a.T = T;
+    a.T = T;
     a.x = x; a.x_f32 = x_type == MOE_F32; a.ldx = ldx;
     a.y = h; a.y_f32 = 1; a.ldy = ldh;
-    return launch(a, gate->fmt, 1, (cudaStream_t)stream);
+    a.status = status;
+    return launch_linear(a, gate, up, (cudaStream_t)stream);
 }
