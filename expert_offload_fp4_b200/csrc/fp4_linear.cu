@@ -25,8 +25,9 @@
 //   warp 1       MMA issuer (owns the TMEM allocation)
 //   warps 1-7    digits of x, first
 //   warps 4-7    epilogue: TMEM -> digit sum -> exchange over the cluster -> y
-//   warps 8-11   one row each: block scales from global memory into the tensor
-//                core's scale-factor layout (see gemm_fp4.cu)
+//   warps 8-11   block scales, one row a thread: global memory -> shared memory ->
+//                TMEM scale columns (tcgen05.st: four tcgen05.cp a stage took as long
+//                as the stage's MMAs)
 // The gated form puts 64 gate rows and the same 64 up rows in one tile.
 // All waits are bounded; a timeout sets bit 16 of *status and the CTA carries on.
 #include "tcgen05.cuh"
@@ -68,17 +69,17 @@ struct LinArgs {
 
 // Shared-memory offsets from the 1024-aligned base.
 struct LinSmem {
-    int codes, atoms, digits, ones, exch, bars, total;
-    __host__ __device__ LinSmem(int stages, int Tp, int Kc, int C, int T, int gated) {
+    int codes, digits, scales, ones, exch, bars, total;
+    __host__ __device__ LinSmem(int stages, int Tp, int Kc, int C, int gated) {
         codes = 0;
         digits = codes + stages * 16384;
-        atoms = digits + Tp * 8 * (Kc / 2);
-        ones = atoms + stages * 2048;
+        scales = digits + Tp * 8 * (Kc / 2);
+        ones = scales + 2 * 2048;
         exch = ones + 512;
         const int out = gated ? 64 : 128, R = (out + C - 1) / C;
-        bars = exch + 2 * 4 * C * (gated ? 2 : 1) * T * R;
+        bars = exch + 2 * 4 * C * (gated ? 2 : 1) * R * (Tp + 2);
         bars = (bars + 15) / 16 * 16;
-        total = bars + (3 * kLinMaxStages + 7) * 8 + 2 * 16 * 4 + 2 * 16 * 4 + 32;
+        total = bars + (2 * kLinMaxStages + 7) * 8 + 48 * 4 + 16;
     }
 };
 
@@ -100,6 +101,17 @@ __device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// 32 lanes x 16 consecutive columns from registers; complete after the wait.
+__device__ __forceinline__ void tmem_st_32x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13,"
+        " %14, %15};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -112,11 +124,14 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Two floats to a CTA of the cluster; the bytes count on that CTA's barrier `bar`.
+__device__ __forceinline__ void st_async_f32x2(uint32_t addr, float v0, float v1, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                 ::"r"(addr), "f"(v0), "f"(v1), "r"(bar) : "memory");
 }
+// Without release: it stands for reads whose values were used already, not for writes.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -200,9 +215,9 @@ __device__ __forceinline__ void digit_rows(const int (&X)[8], uint32_t (&row)[8]
 
 // ---------------------------------------------------------------- block scales
 
-// The scales of one row and stage as 4 words, one per 64 elements: NVFP4 its 4
-// bytes, MXFP4 its 2 in the low half.  p: the stage's first scale of the row, n:
-// how many scales the row has from there (0 for a row or stage outside).
+// The scales of one row and stage: 16 bytes (NVFP4) or 8 (MXFP4, in x and y).  p: the
+// stage's first scale of the row, n: how many scales the row has from there (0 for
+// a row or stage outside).
 template <int FMT>
 __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide) {
     constexpr int per = FMT == MOE_NVFP4 ? 16 : 8;   // scales per stage
@@ -217,8 +232,7 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide)
         for (int i = 0; i < per; i++)
             if (i < n) b[i / 4] |= (uint32_t)__ldg(p + i) << (8 * (i % 4));
     }
-    if constexpr (FMT == MOE_NVFP4) return make_uint4(b[0], b[1], b[2], b[3]);
-    return make_uint4(b[0] & 0xFFFFu, b[0] >> 16, b[1] & 0xFFFFu, b[1] >> 16);
+    return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // ---------------------------------------------------------------- kernel
@@ -230,10 +244,9 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = a.stages, C = a.C, T = a.T, Tp = (T + 1) & ~1;
-    const LinSmem L(S, Tp, a.Kc, C, T, GATED);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars);      // codes landed
-    uint64_t* sfull = full + kLinMaxStages;                         // scales written
-    uint64_t* empty = sfull + kLinMaxStages;                        // stage read by its MMAs
+    const LinSmem L(S, Tp, a.Kc, C, GATED);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars);      // codes landed, scales in TMEM
+    uint64_t* empty = full + kLinMaxStages;                         // stage read by its MMAs
     uint64_t* accf = empty + kLinMaxStages;                         // [2] accumulator complete
     uint64_t* acce = accf + 2;                                      // [2] accumulator read
     uint64_t* exf = acce + 2;                                       // [2] exchange buffer complete
@@ -251,14 +264,13 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&full[s], 1);
-            mbar_init(&sfull[s], 4);
+            mbar_init(&full[s], 1 + 4);
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], 4);
-            mbar_init(&exf[i], 4 * C);
+            mbar_init(&exf[i], 1 + 4 * C);
         }
         mbar_init(bready, kLinPrepWarps);
         fence_mbar_init();
@@ -296,16 +308,16 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int s = 0, ph = 0;
             for (int tile = cl; tile < a.tiles; tile += ncl)
-                for (int kt = 0; kt < KT; kt++, it++) {
-                    const int s = it % S, r = it / S;
-                    if (!mbar_wait(&empty[s], (r & 1) ^ 1, a.limit_ns)) atomicOr(a.status, 1 << 16);
+                for (int kt = 0; kt < KT; kt++) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, a.limit_ns)) atomicOr(a.status, 1 << 16);
                     mbar_arrive_expect_tx(&full[s], 16384);
                     uint8_t* dst = sm + L.codes + s * 16384;
                     const int c0 = k0 / 2 + kt * 128;
                     tma_load_2d(dst, &map0, c0, tile * TR, &full[s]);
                     if (GATED) tma_load_2d(dst + 8192, &map1, c0, tile * TR, &full[s]);
+                    if (++s == S) { s = 0; ph ^= 1; }
                 }
         }
         __syncwarp();
@@ -315,32 +327,55 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         const int pitch = a.K / BS;
         const uint8_t* base = a.m[which].scales + k0 / BS;
         const int have = min(a.K - k0, a.Kc) / BS;       // scales of this CTA's part of a row
-        const int total = cl < a.tiles ? ((a.tiles - cl + ncl - 1) / ncl) * KT : 0;
-        auto fetch = [&](int it) -> uint4 {
-            const int n = (cl + (it / KT) * ncl) * TR + rr, o = (it % KT) * per;
-            const bool in = it < total && n < a.N;
-            return load_scales<FMT>(base + (in ? (size_t)n * pitch + o : 0), in ? have - o : 0, a.wide_scales);
+        const int total = ((a.tiles - cl + ncl - 1) / ncl) * KT;
+        int f_it = 0, f_kt = 0, f_n = cl * TR + rr;      // the next stage to fetch
+        auto fetch = [&]() -> uint4 {
+            const bool in = f_it < total && f_n < a.N;
+            const int o = f_kt * per;
+            const uint4 v = load_scales<FMT>(base + (in ? (size_t)f_n * pitch + o : 0), in ? have - o : 0, a.wide_scales);
+            f_it++;
+            if (++f_kt == KT) {
+                f_kt = 0;
+                f_n += ncl * TR;
+            }
+            return v;
         };
+        const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
         uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) q[i] = fetch(i);
+        for (int i = 0; i < 4; i++) q[i] = fetch();
+        int s = 0, ph = 0;
         for (int it0 = 0; it0 < total; it0 += 4) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int it = it0 + i;
-                if (it < total) {
-                    const int s = it % S;
-                    if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
-                    uint8_t* atom = sm + L.atoms + s * 2048 + 16 * (r & 31) + 4 * (r >> 5);
-                    *reinterpret_cast<uint32_t*>(atom) = q[i].x;
-                    *reinterpret_cast<uint32_t*>(atom + 512) = q[i].y;
-                    *reinterpret_cast<uint32_t*>(atom + 1024) = q[i].z;
-                    *reinterpret_cast<uint32_t*>(atom + 1536) = q[i].w;
-                    fence_proxy_async_smem();
+                if (it0 + i < total) {
+                    // rows to shared memory, then every warp takes all of them for its quarter of
+                    // TMEM's lanes: lane l, column 4 i + j holds step i's scales of row l + 32 j.
+                    // Two buffers and one barrier a stage: a buffer's readers are past the next one
+                    uint8_t* buf = sm + L.scales + (i & 1) * 2048;
+                    *reinterpret_cast<uint4*>(buf + 16 * r) = q[i];
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sfull[s]);
+                    named_sync(2, 128);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(buf + 16 * (lane + 32 * j));
+                        const bool nv = FMT == MOE_NVFP4;
+                        w[j] = nv ? v.x : v.x & 0xFFFFu;
+                        w[4 + j] = nv ? v.y : v.x >> 16;
+                        w[8 + j] = nv ? v.z : v.y & 0xFFFFu;
+                        w[12 + j] = nv ? v.w : v.y >> 16;
+                    }
+                    if (!mbar_wait(&empty[s], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                    __syncwarp();            // the lanes leave the wait one by one
+                    tc_fence_after();
+                    tmem_st_32x16(sf_base + 16 * s + quarter, w);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                    if (++s == S) { s = 0; ph ^= 1; }
                 }
-                q[i] = fetch(it + 4);
+                q[i] = fetch();
             }
         }
     } else {
@@ -355,6 +390,7 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             mx = __reduce_max_sync(0xffffffffu, mx);
             if (lane == 0) atomicMax(&xmax[j / KT], mx);
         }
+        __syncwarp();
         named_sync(1, kLinPrepWarps * 32);
         for (int j = pw; j < items; j += kLinPrepWarps) {
             const int t = j / KT, kt = j % KT;
@@ -391,29 +427,27 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                 tc_fence_after();
                 const uint32_t idesc = idesc_fp4(128, 8 * Tp, FMT == MOE_MXFP4);
                 tmem_cp_sf_atom(sfb, smem_desc(sm + L.ones, 16, 128, 0));
-                int it = 0, tc = 0;
+                const uint64_t ad0 = smem_desc(sm + L.codes, 16, 1024, 2), bd0 = smem_desc(sm + L.digits, 16, 1024, 2);
+                int s = 0, ph = 0, tc = 0;
                 for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
                     const int b = tc & 1;
                     if (!mbar_wait(&acce[b], ((tc >> 1) & 1) ^ 1, a.limit_ns)) atomicOr(a.status, 1 << 16);
-                    tc_fence_after();
                     const uint32_t acc = tbase + b * 8 * Tp;
-                    for (int kt = 0; kt < KT; kt++, it++) {
-                        const int s = it % S, r = it / S;
-                        if (!mbar_wait(&full[s], r & 1, a.limit_ns) || !mbar_wait(&sfull[s], r & 1, a.limit_ns))
-                            atomicOr(a.status, 1 << 16);
+                    for (int kt = 0; kt < KT; kt++) {
+                        if (!mbar_wait(&full[s], ph, a.limit_ns)) atomicOr(a.status, 1 << 16);
                         tc_fence_after();
                         const uint32_t sfa = sf_base + 16 * s;
-                        const int ns = min(4, steps - 4 * kt);
-                        for (int i = 0; i < ns; i++)
-                            tmem_cp_sf_atom(sfa + 4 * i, smem_desc(sm + L.atoms + s * 2048 + 512 * i, 16, 128, 0));
-                        const uint64_t ad = smem_desc(sm + L.codes + s * 16384, 16, 1024, 2);
-                        const uint64_t bd = smem_desc(sm + L.digits + kt * Tp * 1024, 16, 1024, 2);
-                        for (int i = 0; i < ns; i++) {
+                        const uint64_t ad = ad0 + s * (16384 >> 4), bd = bd0 + (uint64_t)(kt * Tp * (1024 >> 4));
+                        const int ns = steps - 4 * kt;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
                             const uint32_t accum = (kt > 0 || i > 0) ? 1u : 0u;
+                            if (i >= ns) break;
                             if (FMT == MOE_NVFP4) mma_nvfp4(acc, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sfb, accum);
                             else mma_mxfp4(acc, ad + 2 * i, bd + 2 * i, idesc, sfa + 4 * i, sfb, accum);
                         }
                         tc_commit(&empty[s]);
+                        if (++s == S) { s = 0; ph ^= 1; }
                     }
                     tc_commit(&accf[b]);
                 }
@@ -426,49 +460,64 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             const int orow = GATED ? row & 63 : row, which = GATED ? row >> 6 : 0;
             const int owner = orow / R;
             constexpr int NW = GATED ? 2 : 1;
-            const int buf_words = C * NW * T * R;
+            const int ldt = Tp + 2;                            // floats per row: pairs stay aligned, few bank conflicts
+            const int buf_words = C * NW * R * ldt;
             const float ts = a.m[which].ts;
             float* exch = reinterpret_cast<float*>(sm + L.exch);
-            // where this row's values go: [src][which][t][row - owner * R] of the owner's buffer
-            const uint32_t dst = (C > 1 ? map_rank(smem_addr(exch), owner) : smem_addr(exch)) +
-                                 4 * ((rank * NW + which) * T * R + orow - owner * R);
-            const int own0 = rank * R, nown = max(0, min(R, TR - own0));
+            // where this row's values go: [src][which][row - owner * R][t] of the owner's buffer
+            const int at = ((rank * NW + which) * R + orow - owner * R) * ldt;
+            const uint32_t dst = map_rank(smem_addr(exch), owner) + 4 * at;
+            const uint32_t dst_bar = map_rank(smem_addr(exf), owner);
+            const uint32_t peer_bar = map_rank(smem_addr(exf), lane < C ? lane : 0);
+            const int own0 = rank * R, nown = min(R, TR - own0);
+            const uint32_t in_bytes = 4 * C * NW * nown * Tp;
+            __syncwarp();
             if (C > 1) cluster_wait();                        // peers' barriers are set
             int tc = 0;
             for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
                 const int b = tc & 1;
+                if (C > 1 && threadIdx.x == 128) mbar_arrive_expect_tx(&exf[b], in_bytes);
                 if (!mbar_wait(&accf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t acc = tbase + b * 8 * Tp + ((uint32_t)(32 * e4) << 16);
-                for (int t0 = 0; t0 < T; t0 += 2) {
+                for (int t0 = 0; t0 < Tp; t0 += 2) {
                     uint32_t d[2][8];
                     tmem_ld_32x8(acc + 8 * t0, d[0]);
                     tmem_ld_32x8(acc + 8 * t0 + 8, d[1]);
                     tmem_ld_wait();
+                    float v[2];
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int t = t0 + h;
-                        if (t >= T) break;
-                        float v = __uint_as_float(d[h][0]);
+                        v[h] = __uint_as_float(d[h][0]);
 #pragma unroll
-                        for (int q = 1; q < 8; q++) v = fmaf(v, 0.125f, __uint_as_float(d[h][q]));
-                        v = v * ts * xscale[t] * xscale[16 + t];
-                        st_cluster_f32(dst + 4 * (b * buf_words + t * R), v);
+                        for (int q = 1; q < 8; q++) v[h] = fmaf(v[h], 0.125f, __uint_as_float(d[h][q]));
+                        v[h] = v[h] * ts * xscale[t0 + h] * xscale[16 + t0 + h];
                     }
+                    if (C > 1) st_async_f32x2(dst + 4 * (b * buf_words + t0), v[0], v[1], dst_bar + 8 * b);
+                    else *reinterpret_cast<float2*>(exch + b * buf_words + at + t0) = make_float2(v[0], v[1]);
+                    __syncwarp();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acce[b]);
-                if (lane < C) mbar_arrive_cluster(C > 1 ? map_rank(smem_addr(&exf[b]), lane) : smem_addr(&exf[b]));
-                if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                if (C > 1) {
+                    // also tells the peers that this warp has read the buffer before this one
+                    if (lane < C) mbar_arrive_cluster(peer_bar + 8 * b);
+                    if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                    __syncwarp();
+                } else {
+                    __syncwarp();
+                    named_sync(3, 128);
+                }
                 const float* in = exch + b * buf_words;
                 for (int j = threadIdx.x - 128; j < T * R; j += 128) {
                     const int t = j / R, o = j - t * R, n = tile * TR + own0 + o;
                     if (o >= nown || n >= a.N) continue;
                     float v = 0.0f, u = 0.0f;
                     for (int c = 0; c < C; c++) {
-                        v += in[c * NW * T * R + j];
-                        if (GATED) u += in[(c * NW + 1) * T * R + j];
+                        v += in[(c * NW * R + o) * ldt + t];
+                        if (GATED) u += in[((c * NW + 1) * R + o) * ldt + t];
                     }
                     if (GATED) v = v / (1.0f + expf(-v)) * u;
                     if (a.add)
@@ -563,8 +612,8 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     const int ncl = std::min(a.tiles, active[a.C]);
     const long long total = (long long)((a.tiles + ncl - 1) / ncl) * kt;
     a.stages = (int)std::min<long long>(kLinMaxStages, total);
-    while (a.stages > 1 && LinSmem(a.stages, Tp, a.Kc, a.C, a.T, GATED).total + 1024 > d.smem) a.stages--;
-    const int smem = LinSmem(a.stages, Tp, a.Kc, a.C, a.T, GATED).total + 1024;
+    while (a.stages > 1 && LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024 > d.smem) a.stages--;
+    const int smem = LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024;
     if (smem > d.smem) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
     const int cols = 2 * 8 * Tp + 16 * a.stages + 4;
     a.tmem_cols = 32;
