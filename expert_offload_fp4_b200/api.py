@@ -136,28 +136,39 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _rows(t, dtypes, shape, what):
+def _rows(t, dtypes, rows, cols, what):
     """Checks a 2-D tensor with contiguous rows; returns its row stride in elements."""
-    _need(t.dtype in dtypes and tuple(t.shape) == shape, f"{what} must be {shape} of {' or '.join(map(str, dtypes))}")
-    _need(t.stride(1) == 1 or shape[1] == 1, f"{what} must have contiguous rows")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    if t.dtype not in dtypes or t.shape != (rows, cols):
+        raise ValueError(f"{what} must be [{rows}, {cols}] of {' or '.join(map(str, dtypes))}")
+    ld, inner = t.stride()
+    if inner != 1 and cols != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return ld if rows > 1 else cols
 
 
 def _call(name, tensors, stream, *args):
     """Library call on the device that holds all of `tensors`, on `stream` or that
     device's current stream."""
     dev = tensors[0].device
-    _need(dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
-          f"{name}: all tensors must be on one CUDA device")
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: all tensors must be on one CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: all tensors must be on one CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _need(stream.device == dev, f"{name}: the stream belongs to another device than the tensors")
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"{name}: the stream belongs to another device than the tensors")
+    else:
+        handle = stream.cuda_stream
     fn = getattr(L.load(), name)
     if torch.cuda.current_device() == dev.index:
-        L.check(name, fn(*args, stream.cuda_stream))
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            L.check(name, fn(*args, stream.cuda_stream))
+            rc = fn(*args, handle)
+    if rc:
+        L.check(name, rc)
 
 
 _SCORE = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
@@ -172,11 +183,11 @@ def _choice(k, score, n_group, topk_group, group_top, renormalize, scale):
 
 def _choice_outputs(T, E, idx, w, bias):
     k = idx.shape[-1]
-    _need(idx.dtype == torch.int32 and tuple(idx.shape) == (T, k) and idx.is_contiguous(),
+    _need(idx.dtype == torch.int32 and idx.shape == (T, k) and idx.is_contiguous(),
           "idx must be a contiguous int32 [T, k]")
-    _need(w.dtype == torch.float32 and tuple(w.shape) == (T, k) and w.is_contiguous(),
+    _need(w.dtype == torch.float32 and w.shape == (T, k) and w.is_contiguous(),
           "w must be a contiguous float32 [T, k]")
-    _need(bias is None or (bias.dtype == torch.float32 and tuple(bias.shape) == (E,) and bias.is_contiguous()),
+    _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous()),
           "bias must be a contiguous float32 [E]")
     return k
 
@@ -211,7 +222,7 @@ def route_select(logits, idx, w, *, score="sigmoid", bias=None, n_group=1, topk_
     with any row stride (a logit of -inf masks its expert)."""
     _need(logits.dim() == 2, "logits must be [T, E]")
     T, E = logits.shape
-    ld = _rows(logits, tuple(_TYPE), (T, E), "logits")
+    ld = _rows(logits, _TYPE, T, E, "logits")
     k = _choice_outputs(T, E, idx, w, bias)
     _call("moe_route_select", (logits, idx, w, bias), stream, logits.data_ptr(), _TYPE[logits.dtype], ld,
           None if bias is None else bias.data_ptr(), T, E,
@@ -250,9 +261,9 @@ def fp4_linear(x, weight, y, status, add=None, stream=None):
     T <= 16.  add: None or like y (it may be y itself).  Row strides are free."""
     _need(x.dim() == 2, "x must be [T, K]")
     T = x.shape[0]
-    ldx = _rows(x, tuple(_TYPE), (T, weight.K), "x")
-    ldy = _rows(y, tuple(_TYPE), (T, weight.N), "y")
-    lda = 0 if add is None else _rows(add, (y.dtype,), (T, weight.N), "add")
+    ldx = _rows(x, _TYPE, T, weight.K, "x")
+    ldy = _rows(y, _TYPE, T, weight.N, "y")
+    lda = 0 if add is None else _rows(add, (y.dtype,), T, weight.N, "add")
     _call("moe_fp4_linear", (x, weight.codes, y, status, add), stream, weight.ref, x.data_ptr(), _TYPE[x.dtype], ldx,
           T, None if add is None else add.data_ptr(), lda, y.data_ptr(), _TYPE[y.dtype], ldy, _status(status))
 
@@ -261,8 +272,8 @@ def fp4_swiglu(x, gate, up, h, status, stream=None):
     """moe_fp4_swiglu: h [T, N] fp32 = silu(x W_gate^T) * (x W_up^T), T <= 16."""
     _need(x.dim() == 2, "x must be [T, K]")
     T = x.shape[0]
-    ldx = _rows(x, tuple(_TYPE), (T, gate.K), "x")
-    ldh = _rows(h, (torch.float32,), (T, gate.N), "h")
+    ldx = _rows(x, _TYPE, T, gate.K, "x")
+    ldh = _rows(h, (torch.float32,), T, gate.N, "h")
     _call("moe_fp4_swiglu", (x, gate.codes, up.codes, h, status), stream, gate.ref, up.ref, x.data_ptr(),
           _TYPE[x.dtype], ldx, T, h.data_ptr(), ldh, _status(status))
 

@@ -23,8 +23,10 @@
 // not depend on timing.  Warp roles:
 //   warp 0       TMA producer: a 128-row x 256-element code tile per stage
 //   warp 1       MMA issuer (owns the TMEM allocation)
-//   warps 1-7    digits of x, first
-//   warps 4-7    epilogue: TMEM -> digit sum -> exchange over the cluster -> y
+//   warps 1-11   digits of x, first
+//   warps 2-3    exchange buffer -> sum over the cluster -> y, one tile behind the
+//                drain, so that neither waits for the other
+//   warps 4-7    drain: TMEM -> digit sum -> the owner's exchange buffer
 //   warps 8-11   block scales, one row a thread: global memory -> shared memory ->
 //                TMEM scale columns (tcgen05.st: four tcgen05.cp a stage took as long
 //                as the stage's MMAs)
@@ -41,7 +43,8 @@ constexpr int kLinThreads = 384;
 constexpr int kLinKT = 256;               // K elements of a stage (128 code bytes a row)
 constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxCluster = 8;
-constexpr int kLinPrepWarps = 7;          // warps 1 .. 7
+constexpr int kLinPrepWarps = 11;         // warps 1 .. 11
+constexpr int kLinSumThreads = 64;        // warps 2, 3
 
 struct LinMat {
     const uint8_t* scales;
@@ -67,6 +70,10 @@ struct LinArgs {
     unsigned long long limit_ns;
 };
 
+// Floats of one row's values in the exchange buffer: its tokens in fours, and four
+// more so that the rows of a quarter warp fall into different banks.
+__host__ __device__ constexpr int lin_row_words(int Tp) { return (Tp + 3) / 4 * 4 + 4; }
+
 // Shared-memory offsets from the 1024-aligned base.
 struct LinSmem {
     int codes, digits, scales, ones, exch, bars, total;
@@ -77,9 +84,9 @@ struct LinSmem {
         ones = scales + 2 * 2048;
         exch = ones + 512;
         const int out = gated ? 64 : 128, R = (out + C - 1) / C;
-        bars = exch + 2 * 4 * C * (gated ? 2 : 1) * R * (Tp + 2);
+        bars = exch + 2 * 4 * C * (gated ? 2 : 1) * R * lin_row_words(Tp);
         bars = (bars + 15) / 16 * 16;
-        total = bars + (2 * kLinMaxStages + 7) * 8 + 48 * 4 + 16;
+        total = bars + (2 * kLinMaxStages + 9) * 8 + 48 * 4 + 16;
     }
 };
 
@@ -124,10 +131,10 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
     return a;
 }
-// Two floats to a CTA of the cluster; the bytes count on that CTA's barrier `bar`.
-__device__ __forceinline__ void st_async_f32x2(uint32_t addr, float v0, float v1, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
-                 ::"r"(addr), "f"(v0), "f"(v1), "r"(bar) : "memory");
+// Four floats to a CTA of the cluster; the bytes count on that CTA's barrier `bar`.
+__device__ __forceinline__ void st_async_f32x4(uint32_t addr, const float (&v)[4], uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(bar) : "memory");
 }
 // Without release: it stands for reads whose values were used already, not for writes.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -161,38 +168,49 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 
 // ---------------------------------------------------------------- x digits
 
-// 8 consecutive elements of row t from k (k % 8 == 0); zeros from K on.
-__device__ __forceinline__ void load_x8(const LinArgs& a, int t, int k, float (&v)[8]) {
-    if (t >= a.T || k >= a.K) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = 0.0f;
-    } else if (a.x_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + t * a.ldx + k);
-        const float4 p0 = p[0], p1 = p[1];
-        v[0] = p0.x; v[1] = p0.y; v[2] = p0.z; v[3] = p0.w;
-        v[4] = p1.x; v[5] = p1.y; v[6] = p1.z; v[7] = p1.w;
-    } else {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.ldx + k);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+// 8 consecutive elements of x, as they are in memory (k % 8 == 0); zeros from K on.
+template <int XF32>
+struct X8 {
+    uint4 q[XF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const LinArgs& a, int t, int k) {
+        q[0] = make_uint4(0, 0, 0, 0);
+        if (XF32) q[XF32] = q[0];
+        if (t >= a.T || k >= a.K) return;
+        if (XF32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + t * a.ldx + k);
+            q[0] = p[0];
+            q[XF32] = p[1];
+        } else {
+            q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.ldx + k);
         }
     }
-}
+    __device__ __forceinline__ void put(uint8_t* p, int lane) const {
+        reinterpret_cast<uint4*>(p)[lane] = q[0];
+        if (XF32) reinterpret_cast<uint4*>(p)[32 + lane] = q[XF32];
+    }
+    __device__ __forceinline__ void get(const uint8_t* p, int lane) {
+        q[0] = reinterpret_cast<const uint4*>(p)[lane];
+        if (XF32) q[XF32] = reinterpret_cast<const uint4*>(p)[32 + lane];
+    }
+    __device__ __forceinline__ uint32_t bits(int i) const {   // element i as fp32
+        const uint4& v = q[XF32 ? i >> 2 : 0];
+        const int j = XF32 ? i & 3 : i >> 1;
+        const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+        return XF32 ? w : (i & 1) ? w & 0xFFFF0000u : w << 16;
+    }
+};
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// X (|X| <= 2^22) as 8 selector nibbles u_d + 4, the lowest digit in the lowest nibble.
-__device__ __forceinline__ uint32_t octal_nibbles(int X) {
-    const uint32_t u = (uint32_t)(X + 0x924924);          // 4 (8^8 - 1) / 7
-    const uint32_t w = (u & 0xFFFu) | ((u & 0xFFF000u) << 4);
-    return (w & 0x00070007u) | ((w & 0x00380038u) << 1) | ((w & 0x01C001C0u) << 2) | ((w & 0x0E000E00u) << 3);
+// X + 4 (8^8 - 1) / 7, whose plain octal digits are u_d + 4, as 8 selector nibbles, the
+// lowest digit in the lowest nibble.
+__device__ __forceinline__ uint32_t octal_nibbles(uint32_t u) {
+    const uint32_t w = (u & 0xFFFu) + (u & 0xFFF000u) * 16u;
+    return (w & 0x00070007u) + (w & 0x00380038u) * 2u + (w & 0x01C001C0u) * 4u + (w & 0x0E000E00u) * 8u;
 }
 
 // 8 elements -> for each digit d the 4 bytes (8 codes) of B's row d.
-__device__ __forceinline__ void digit_rows(const int (&X)[8], uint32_t (&row)[8]) {
+__device__ __forceinline__ void digit_rows(const uint32_t (&X)[8], uint32_t (&row)[8]) {
     // E2M1 codes of -4 -3 -2 -1 | 0 1 2 3, and the same in the high nibble
     constexpr uint32_t la = 0x0A0C0D0Eu, lb = 0x05040200u, ha = la << 4, hb = lb << 4;
     uint32_t p[2][4];
@@ -237,8 +255,8 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide)
 
 // ---------------------------------------------------------------- kernel
 
-template <int FMT, int GATED>
-__global__ void __launch_bounds__(kLinThreads, 1)
+template <int FMT, int GATED, int XF32>
+__global__ void __launch_bounds__(kLinThreads, 2)
 fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                   const LinArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -250,7 +268,8 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     uint64_t* accf = empty + kLinMaxStages;                         // [2] accumulator complete
     uint64_t* acce = accf + 2;                                      // [2] accumulator read
     uint64_t* exf = acce + 2;                                       // [2] exchange buffer complete
-    uint64_t* bready = exf + 2;                                     // digits of x complete
+    uint64_t* exe = exf + 2;                                        // [2] this CTA's values read by their owners
+    uint64_t* bready = exe + 2;                                     // digits of x complete
     uint32_t* xmax = reinterpret_cast<uint32_t*>(bready + 1);       // [16] largest |x| bits, then 2 x [16] 2^E
     float* xscale = reinterpret_cast<float*>(xmax + 16);
     uint32_t* tmem_slot = xmax + 48;
@@ -270,7 +289,8 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         for (int i = 0; i < 2; i++) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], 4);
-            mbar_init(&exf[i], 1 + 4 * C);
+            mbar_init(&exf[i], C > 1 ? 1 : 4);
+            mbar_init(&exe[i], kLinSumThreads / 32 * C);
         }
         mbar_init(bready, kLinPrepWarps);
         fence_mbar_init();
@@ -306,6 +326,71 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     }
     pdl_wait();
 
+    auto digits_of_x = [&]() {
+        // digits of x: items are (token, 256 elements), 8 elements per lane.  An item's 1 KiB of
+        // digits first holds its elements as loaded; the same warp turns them into digits once
+        // the tokens' largest elements are known.  Short loops, not unrolled copies: a CTA runs
+        // this once, at the speed at which it can fetch the instructions
+        const int pw = warp - 1, items = Tp * KT;
+        uint8_t* digits = sm + L.digits;                  // item (t, kt) at (kt * Tp + t) KiB
+        constexpr int batch = XF32 ? 3 : 6;
+        for (int j0 = pw; j0 < items; j0 += batch * kLinPrepWarps) {
+            X8<XF32> v[batch];
+#pragma unroll
+            for (int i = 0; i < batch; i++) {
+                const int j = j0 + i * kLinPrepWarps, kt = j / Tp;
+                v[i].load(a, j < items ? j - kt * Tp : T, k0 + kt * kLinKT + lane * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < batch; i++) {
+                const int j = j0 + i * kLinPrepWarps;
+                if (j >= items) break;
+                v[i].put(digits + j * 1024, lane);
+                uint32_t mx = 0;
+#pragma unroll
+                for (int e = 0; e < 8; e++) mx = max(mx, v[i].bits(e) & 0x7FFFFFFFu);
+                mx = __reduce_max_sync(0xffffffffu, mx);
+                if (lane == 0) atomicMax(&xmax[j % Tp], mx);
+            }
+        }
+        __syncwarp();
+        named_sync(1, kLinPrepWarps * 32);
+#pragma unroll 1
+        for (int j = pw; j < items; j += kLinPrepWarps) {
+            const int t = j % Tp;
+            const uint32_t mx = xmax[t];
+            // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
+            const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
+            const bool finite = mx < 0x7F800000u;
+            const int up = 21 - E, h1 = up / 2, d1 = E / 2;
+            const float f1 = exp2i(h1), f2 = exp2i(up - h1);
+            uint8_t* dst = digits + j * 1024;
+            X8<XF32> v;
+            v.get(dst, lane);
+            // rounded by adding 1.5 2^23, whose bits X then counts from
+            uint32_t X[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                X[e] = __float_as_uint(fmaf(__uint_as_float(v.bits(e)) * f1, f2, 12582912.0f)) - 0x4B400000u + 0x924924u;
+            uint32_t row[8];
+            digit_rows(X, row);
+            __syncwarp();                                 // all lanes have their elements
+            // rows 8 t + d of the K-major operand, 128-byte swizzle: 16-byte chunk c of row d at c ^ d
+#pragma unroll
+            for (int d = 0; d < 8; d++)
+                *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = row[d];
+            if (j < Tp && lane == 0) {
+                xscale[t] = finite ? exp2i(d1) : __uint_as_float(0x7FC00000u);
+                xscale[16 + t] = exp2i(E - d1);
+            }
+        }
+        // (the MMA thread orders these stores before its reads: a proxy fence here would wait
+        // for warps 8-11's loads of scales)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bready);
+        __syncwarp();
+    };
+
     if (warp == 0) {
         if (lane == 0) {
             int s = 0, ph = 0;
@@ -322,13 +407,14 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         }
         __syncwarp();
     } else if (warp >= 8) {
-        const int r = threadIdx.x - 256, which = GATED ? r >> 6 : 0, rr = GATED ? r & 63 : r;
+        // block scales: thread r of warps 8-11 fetches row r's, a few stages ahead
+        const int r = threadIdx.x & 127, which_r = GATED ? r >> 6 : 0;
         constexpr int BS = FMT == MOE_NVFP4 ? 16 : 32, per = kLinKT / BS;
         const int pitch = a.K / BS;
-        const uint8_t* base = a.m[which].scales + k0 / BS;
+        const uint8_t* base = a.m[which_r].scales + k0 / BS;
         const int have = min(a.K - k0, a.Kc) / BS;       // scales of this CTA's part of a row
         const int total = ((a.tiles - cl + ncl - 1) / ncl) * KT;
-        int f_it = 0, f_kt = 0, f_n = cl * TR + rr;      // the next stage to fetch
+        int f_it = 0, f_kt = 0, f_n = cl * TR + (GATED ? r & 63 : r);      // the next stage to fetch
         auto fetch = [&]() -> uint4 {
             const bool in = f_it < total && f_n < a.N;
             const int o = f_kt * per;
@@ -340,10 +426,11 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             }
             return v;
         };
-        const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
         uint4 q[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) q[i] = fetch();
+        digits_of_x();
+        const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
         int s = 0, ph = 0;
         for (int it0 = 0; it0 < total; it0 += 4) {
 #pragma unroll
@@ -359,12 +446,12 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(buf + 16 * (lane + 32 * j));
+                        const uint4 u = *reinterpret_cast<const uint4*>(buf + 16 * (lane + 32 * j));
                         const bool nv = FMT == MOE_NVFP4;
-                        w[j] = nv ? v.x : v.x & 0xFFFFu;
-                        w[4 + j] = nv ? v.y : v.x >> 16;
-                        w[8 + j] = nv ? v.z : v.y & 0xFFFFu;
-                        w[12 + j] = nv ? v.w : v.y >> 16;
+                        w[j] = nv ? u.x : u.x & 0xFFFFu;
+                        w[4 + j] = nv ? u.y : u.x >> 16;
+                        w[8 + j] = nv ? u.z : u.y & 0xFFFFu;
+                        w[12 + j] = nv ? u.w : u.y >> 16;
                     }
                     if (!mbar_wait(&empty[s], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
                     __syncwarp();            // the lanes leave the wait one by one
@@ -379,51 +466,19 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             }
         }
     } else {
-        // digits of x: items are (token, 256 elements), 8 elements per lane
-        const int pw = warp - 1, items = Tp * KT;
-        for (int j = pw; j < items; j += kLinPrepWarps) {
-            float v[8];
-            load_x8(a, j / KT, k0 + (j % KT) * kLinKT + lane * 8, v);
-            uint32_t mx = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) mx = max(mx, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-            mx = __reduce_max_sync(0xffffffffu, mx);
-            if (lane == 0) atomicMax(&xmax[j / KT], mx);
-        }
+        digits_of_x();
+
+        const int R = (TR + C - 1) / C;                   // output rows per owner
+        constexpr int NW = GATED ? 2 : 1;
+        const int ldt = lin_row_words(Tp);
+        const int buf_words = C * NW * R * ldt;           // [src][which][row - owner * R][t]
+        float* exch = reinterpret_cast<float*>(sm + L.exch);
         __syncwarp();
-        named_sync(1, kLinPrepWarps * 32);
-        for (int j = pw; j < items; j += kLinPrepWarps) {
-            const int t = j / KT, kt = j % KT;
-            const uint32_t mx = xmax[t];
-            // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
-            const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
-            const bool finite = mx < 0x7F800000u;
-            const int up = 21 - E, h1 = up / 2, d1 = E / 2;
-            const float f1 = exp2i(h1), f2 = exp2i(up - h1);
-            float v[8];
-            load_x8(a, t, k0 + kt * kLinKT + lane * 8, v);
-            int X[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) X[i] = finite ? __float2int_rn(v[i] * f1 * f2) : 0;
-            uint32_t row[8];
-            digit_rows(X, row);
-            // rows 8 t + d of the K-major operand, 128-byte swizzle: 16-byte chunk c of row d at c ^ d
-            uint8_t* dst = sm + L.digits + (kt * Tp + t) * 1024;
-#pragma unroll
-            for (int d = 0; d < 8; d++)
-                *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = row[d];
-            if (kt == 0 && lane == 0) {
-                xscale[t] = finite ? exp2i(d1) : __uint_as_float(0x7FC00000u);
-                xscale[16 + t] = exp2i(E - d1);
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bready);
 
         if (warp == 1) {
             if (lane == 0) {
                 if (!mbar_wait(bready, 0, a.limit_ns)) atomicOr(a.status, 1 << 16);
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t idesc = idesc_fp4(128, 8 * Tp, FMT == MOE_MXFP4);
                 tmem_cp_sf_atom(sfb, smem_desc(sm + L.ones, 16, 128, 0));
@@ -456,84 +511,120 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         } else if (warp >= 4) {
             if (!mbar_wait(bready, 0, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);   // xscale
             const int e4 = warp - 4, row = 32 * e4 + lane;
-            const int R = (TR + C - 1) / C;                   // output rows per owner
             const int orow = GATED ? row & 63 : row, which = GATED ? row >> 6 : 0;
             const int owner = orow / R;
-            constexpr int NW = GATED ? 2 : 1;
-            const int ldt = Tp + 2;                            // floats per row: pairs stay aligned, few bank conflicts
-            const int buf_words = C * NW * R * ldt;
             const float ts = a.m[which].ts;
-            float* exch = reinterpret_cast<float*>(sm + L.exch);
-            // where this row's values go: [src][which][row - owner * R][t] of the owner's buffer
             const int at = ((rank * NW + which) * R + orow - owner * R) * ldt;
             const uint32_t dst = map_rank(smem_addr(exch), owner) + 4 * at;
             const uint32_t dst_bar = map_rank(smem_addr(exf), owner);
-            const uint32_t peer_bar = map_rank(smem_addr(exf), lane < C ? lane : 0);
-            const int own0 = rank * R, nown = min(R, TR - own0);
-            const uint32_t in_bytes = 4 * C * NW * nown * Tp;
             __syncwarp();
             if (C > 1) cluster_wait();                        // peers' barriers are set
             int tc = 0;
             for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
-                const int b = tc & 1;
-                if (C > 1 && threadIdx.x == 128) mbar_arrive_expect_tx(&exf[b], in_bytes);
-                if (!mbar_wait(&accf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                const int b = tc & 1, ph = (tc >> 1) & 1;
+                if (!mbar_wait(&exe[b], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                if (!mbar_wait(&accf[b], ph, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t acc = tbase + b * 8 * Tp + ((uint32_t)(32 * e4) << 16);
-                for (int t0 = 0; t0 < Tp; t0 += 2) {
-                    uint32_t d[2][8];
+#pragma unroll 1
+                for (int t0 = 0; t0 < Tp; t0 += 4) {
+                    uint32_t d[4][8];
+                    const bool four = Tp - t0 >= 4;
                     tmem_ld_32x8(acc + 8 * t0, d[0]);
                     tmem_ld_32x8(acc + 8 * t0 + 8, d[1]);
-                    tmem_ld_wait();
-                    float v[2];
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        v[h] = __uint_as_float(d[h][0]);
-#pragma unroll
-                        for (int q = 1; q < 8; q++) v[h] = fmaf(v[h], 0.125f, __uint_as_float(d[h][q]));
-                        v[h] = v[h] * ts * xscale[t0 + h] * xscale[16 + t0 + h];
+                    if (four) {
+                        tmem_ld_32x8(acc + 8 * t0 + 16, d[2]);
+                        tmem_ld_32x8(acc + 8 * t0 + 24, d[3]);
                     }
-                    if (C > 1) st_async_f32x2(dst + 4 * (b * buf_words + t0), v[0], v[1], dst_bar + 8 * b);
-                    else *reinterpret_cast<float2*>(exch + b * buf_words + at + t0) = make_float2(v[0], v[1]);
+                    tmem_ld_wait();
+                    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int h = 0; h < 4; h++) {
+                        if (h >= 2 && !four) break;
+                        o[h] = __uint_as_float(d[h][0]);
+#pragma unroll
+                        for (int g = 1; g < 8; g++) o[h] = fmaf(o[h], 0.125f, __uint_as_float(d[h][g]));
+                        o[h] = o[h] * ts * xscale[t0 + h] * xscale[16 + t0 + h];
+                    }
+                    if (C > 1) st_async_f32x4(dst + 4 * (b * buf_words + t0), o, dst_bar + 8 * b);
+                    else *reinterpret_cast<float4*>(exch + b * buf_words + at + t0) = make_float4(o[0], o[1], o[2], o[3]);
                     __syncwarp();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acce[b]);
-                if (C > 1) {
-                    // also tells the peers that this warp has read the buffer before this one
-                    if (lane < C) mbar_arrive_cluster(peer_bar + 8 * b);
-                    if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
-                    __syncwarp();
-                } else {
-                    __syncwarp();
-                    named_sync(3, 128);
-                }
-                const float* in = exch + b * buf_words;
-                for (int j = threadIdx.x - 128; j < T * R; j += 128) {
-                    const int t = j / R, o = j - t * R, n = tile * TR + own0 + o;
-                    if (o >= nown || n >= a.N) continue;
-                    float v = 0.0f, u = 0.0f;
-                    for (int c = 0; c < C; c++) {
-                        v += in[(c * NW * R + o) * ldt + t];
-                        if (GATED) u += in[((c * NW + 1) * R + o) * ldt + t];
-                    }
-                    if (GATED) v = v / (1.0f + expf(-v)) * u;
-                    if (a.add)
-                        v += a.y_f32 ? static_cast<const float*>(a.add)[t * a.ld_add + n]
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.add)[t * a.ld_add + n]);
-                    if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
-                    else static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + n] = __float2bfloat16_rn(v);
+                if (lane == 0) {
+                    mbar_arrive(&acce[b]);
+                    if (C == 1) mbar_arrive(&exf[b]);
                 }
             }
+            __syncwarp();
+            if (C > 1) cluster_arrive();
+        } else {
+            const int tid = threadIdx.x - 64;
+            const uint32_t peer_exe = map_rank(smem_addr(exe), lane < C ? lane : 0);
+            const int own0 = rank * R, nown = min(R, TR - own0);
+            const int quads = (T + 3) / 4;                    // a thread sums one row of four tokens
+            const uint32_t in_bytes = 16 * C * NW * nown * quads;
+            const int src_words = NW * R * ldt;
+            if (C > 1) cluster_wait();
+            int tc = 0;
+            for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
+                const int b = tc & 1;
+                if (C > 1 && tid == 0) mbar_arrive_expect_tx(&exf[b], in_bytes);
+                if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                __syncwarp();
+                if (C > 1 && tile + ncl >= a.tiles) cluster_arrive();   // no more access to peers from here
+#pragma unroll 1
+                for (int j = tid; j < quads * R; j += kLinSumThreads) {
+                    const int g = j / R, o = j - g * R, n = tile * TR + own0 + o;
+                    if (o >= nown || n >= a.N) continue;
+                    const float* in = exch + b * buf_words + o * ldt + 4 * g;
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                    for (int c = 0; c < C; c++, in += src_words) {
+                        const float4 p = *reinterpret_cast<const float4*>(in);
+                        y[0] += p.x; y[1] += p.y; y[2] += p.z; y[3] += p.w;
+                        if (GATED) {
+                            const float4 q = *reinterpret_cast<const float4*>(in + R * ldt);
+                            u[0] += q.x; u[1] += q.y; u[2] += q.z; u[3] += q.w;
+                        }
+                    }
+                    const int nt = min(4, T - 4 * g);
+#pragma unroll
+                    for (int h = 0; h < 4; h++) {
+                        if (h >= nt) break;
+                        float v = y[h];
+                        const long long t = 4 * g + h;
+                        if (GATED) v = v / (1.0f + expf(-v)) * u[h];
+                        if (a.add)
+                            v += a.y_f32 ? static_cast<const float*>(a.add)[t * a.ld_add + n]
+                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.add)[t * a.ld_add + n]);
+                        if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
+                        else static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + n] = __float2bfloat16_rn(v);
+                    }
+                }
+                __syncwarp();
+                // the buffer may be written again, if another tile will use it
+                if (tile + 2 * ncl < a.tiles) {
+                    if (C > 1) {
+                        if (lane < C) mbar_arrive_cluster(peer_exe + 8 * b);
+                    } else if (lane == 0) {
+                        mbar_arrive(&exe[b]);
+                    }
+                }
+            }
+            __syncwarp();
         }
     }
-    // the cluster's CTAs leave together: none may end while a peer still writes to it
+    // No CTA of a cluster ends while a peer may still write to it.  Warps 4-7 arrived after
+    // their last store to a peer, warps 2-3 after their last wait
     if (C > 1) {
         __syncwarp();
-        if (warp < 4 || warp >= 8) cluster_wait();   // the epilogue warps waited above
-        cluster_arrive();
+        if (warp < 2 || warp >= 8) {
+            cluster_wait();
+            cluster_arrive();
+        }
         cluster_wait();
     }
     __syncthreads();
@@ -565,15 +656,15 @@ static int check_rows(const void* p, int type, long long ld, int width, int T, c
 struct LinDevice {
     int sms = 0;
     int smem = 0;                              // dynamic shared memory a block may take
-    int clusters[4][kLinMaxCluster + 1] = {};  // co-resident clusters per kernel and cluster size
+    int clusters[8][kLinMaxCluster + 1] = {};  // co-resident clusters per kernel and cluster size
 };
 
-template <int FMT, int GATED>
+template <int FMT, int GATED, int XF32>
 static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& m1, LinDevice& d, cudaStream_t s) {
-    auto kern = fp4_linear_kernel<FMT, GATED>;
+    auto kern = fp4_linear_kernel<FMT, GATED, XF32>;
     const int Tp = (a.T + 1) & ~1, KTall = (a.K + kLinKT - 1) / kLinKT;
     a.tiles = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
-    int* active = d.clusters[FMT * 2 + GATED];
+    int* active = d.clusters[FMT * 4 + GATED * 2 + XF32];
     if (!active[1]) {
         MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem));
         for (int C = kLinMaxCluster; C >= 1; C--) {
@@ -675,11 +766,17 @@ static int launch_linear(LinArgs& a, const moe_fp4_weight* w0, const moe_fp4_wei
     }
     if (!w1) maps[1] = maps[0];
     a.wide_scales = low % (w0->fmt == MOE_NVFP4 ? 16 : 8) == 0;
-    if (w0->fmt == MOE_NVFP4)
-        return w1 ? launch_variant<MOE_NVFP4, 1>(a, maps[0], maps[1], *d, s)
-                  : launch_variant<MOE_NVFP4, 0>(a, maps[0], maps[1], *d, s);
-    return w1 ? launch_variant<MOE_MXFP4, 1>(a, maps[0], maps[1], *d, s)
-              : launch_variant<MOE_MXFP4, 0>(a, maps[0], maps[1], *d, s);
+    const int v = (w0->fmt == MOE_NVFP4 ? 4 : 0) + (w1 ? 2 : 0) + (a.x_f32 ? 1 : 0);
+    switch (v) {
+        case 0: return launch_variant<MOE_MXFP4, 0, 0>(a, maps[0], maps[1], *d, s);
+        case 1: return launch_variant<MOE_MXFP4, 0, 1>(a, maps[0], maps[1], *d, s);
+        case 2: return launch_variant<MOE_MXFP4, 1, 0>(a, maps[0], maps[1], *d, s);
+        case 3: return launch_variant<MOE_MXFP4, 1, 1>(a, maps[0], maps[1], *d, s);
+        case 4: return launch_variant<MOE_NVFP4, 0, 0>(a, maps[0], maps[1], *d, s);
+        case 5: return launch_variant<MOE_NVFP4, 0, 1>(a, maps[0], maps[1], *d, s);
+        case 6: return launch_variant<MOE_NVFP4, 1, 0>(a, maps[0], maps[1], *d, s);
+        default: return launch_variant<MOE_NVFP4, 1, 1>(a, maps[0], maps[1], *d, s);
+    }
 }
 
 }  // namespace moe
