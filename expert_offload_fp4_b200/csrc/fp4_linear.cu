@@ -23,7 +23,7 @@
 // not depend on timing.  Warp roles:
 //   warp 0       TMA producer: a 128-row x 256-element code tile per stage
 //   warp 1       MMA issuer (owns the TMEM allocation)
-//   warps 1-11   digits of x, first
+//   warps 1-7    digits of x, first (1-11 where there are many)
 //   warps 2-3    exchange buffer -> sum over the cluster -> y, one tile behind the
 //                drain, so that neither waits for the other
 //   warps 4-7    drain: TMEM -> digit sum -> the owner's exchange buffer
@@ -43,7 +43,6 @@ constexpr int kLinThreads = 384;
 constexpr int kLinKT = 256;               // K elements of a stage (128 code bytes a row)
 constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxCluster = 8;
-constexpr int kLinPrepWarps = 11;         // warps 1 .. 11
 constexpr int kLinSumThreads = 64;        // warps 2, 3
 
 struct LinMat {
@@ -59,6 +58,7 @@ struct LinArgs {
     int tiles;
     int wide_scales;     // scale rows can be read 16 (NVFP4) or 8 (MXFP4) bytes at a time
     uint32_t tmem_cols;
+    int tp_inv, r_inv;   // ceil(65536 / x) of Tp and of the output rows per owner, for small quotients
     int x_f32, y_f32;
     const void* x;
     long long ldx;
@@ -76,17 +76,18 @@ __host__ __device__ constexpr int lin_row_words(int Tp) { return (Tp + 3) / 4 * 
 
 // Shared-memory offsets from the 1024-aligned base.
 struct LinSmem {
-    int codes, digits, scales, ones, exch, bars, total;
+    int codes, digits, scales, ones, exch, bars, args, total;
     __host__ __device__ LinSmem(int stages, int Tp, int Kc, int C, int gated) {
         codes = 0;
         digits = codes + stages * 16384;
         scales = digits + Tp * 8 * (Kc / 2);
-        ones = scales + 2 * 2048;
+        ones = scales + 4 * 2048;
         exch = ones + 512;
         const int out = gated ? 64 : 128, R = (out + C - 1) / C;
         bars = exch + 2 * 4 * C * (gated ? 2 : 1) * R * lin_row_words(Tp);
-        bars = (bars + 15) / 16 * 16;
-        total = bars + (2 * kLinMaxStages + 9) * 8 + 48 * 4 + 16;
+        bars = (bars + 15) / 16 * 16;   // (and the arguments after the barriers 8-byte aligned)
+        args = bars + (2 * kLinMaxStages + 9) * 8 + 48 * 4 + 16;
+        total = args + (int)sizeof(LinArgs);
     }
 };
 
@@ -116,8 +117,8 @@ __device__ __forceinline__ void tmem_st_32x16(uint32_t taddr, const uint32_t (&r
         ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
           "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- cluster
 
@@ -141,6 +142,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
@@ -168,21 +170,16 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 
 // ---------------------------------------------------------------- x digits
 
-// 8 consecutive elements of x, as they are in memory (k % 8 == 0); zeros from K on.
+// 8 consecutive elements of x, as they are in memory.
 template <int XF32>
 struct X8 {
     uint4 q[XF32 ? 2 : 1];
-    __device__ __forceinline__ void load(const LinArgs& a, int t, int k) {
+    __device__ __forceinline__ void load(const void* x, bool in) {   // zeros if not in
         q[0] = make_uint4(0, 0, 0, 0);
         if (XF32) q[XF32] = q[0];
-        if (t >= a.T || k >= a.K) return;
-        if (XF32) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + t * a.ldx + k);
-            q[0] = p[0];
-            q[XF32] = p[1];
-        } else {
-            q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.ldx + k);
-        }
+        if (!in) return;
+        q[0] = static_cast<const uint4*>(x)[0];
+        if (XF32) q[XF32] = static_cast<const uint4*>(x)[XF32];
     }
     __device__ __forceinline__ void put(uint8_t* p, int lane) const {
         reinterpret_cast<uint4*>(p)[lane] = q[0];
@@ -258,11 +255,15 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide)
 template <int FMT, int GATED, int XF32>
 __global__ void __launch_bounds__(kLinThreads, 2)
 fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
-                  const LinArgs a) {
+                  const __grid_constant__ LinArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int S = a.stages, C = a.C, T = a.T, Tp = (T + 1) & ~1;
-    const LinSmem L(S, Tp, a.Kc, C, GATED);
+    const int S = args.stages, C = args.C, T = args.T, Tp = (T + 1) & ~1;
+    const LinSmem L(S, Tp, args.Kc, C, GATED);
+    // the arguments once more in shared memory: read late for the first time, each line of
+    // the constant bank is a miss of several hundred cycles
+    const LinArgs& a = *reinterpret_cast<const LinArgs*>(sm + L.args);
+    static_assert(sizeof(LinArgs) % 8 == 0 && sizeof(LinArgs) / 4 <= kLinThreads, "");
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars);      // codes landed, scales in TMEM
     uint64_t* empty = full + kLinMaxStages;                         // stage read by its MMAs
     uint64_t* accf = empty + kLinMaxStages;                         // [2] accumulator complete
@@ -276,10 +277,12 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int cl = blockIdx.x / C, ncl = gridDim.x / C;
-    const int k0 = rank * a.Kc;
-    const int steps = (min(a.K - k0, a.Kc) + 63) / 64;              // 64-element MMA steps of this CTA
+    const int k0 = rank * args.Kc;
+    const int steps = (min(args.K - k0, args.Kc) + 63) / 64;              // 64-element MMA steps of this CTA
     const int KT = (steps + 3) / 4;                                 // stages per tile
     constexpr int TR = GATED ? 64 : 128;                            // rows of each matrix per tile
+    // the scale warps help with the digits only where there are many
+    const int items = Tp * KT, nprep = items > 21 ? 11 : 7;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
@@ -292,15 +295,17 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             mbar_init(&exf[i], C > 1 ? 1 : 4);
             mbar_init(&exe[i], kLinSumThreads / 32 * C);
         }
-        mbar_init(bready, kLinPrepWarps);
+        mbar_init(bready, nprep);
         fence_mbar_init();
         prefetch_tmap(&map0);
         if (GATED) prefetch_tmap(&map1);
     }
+    if (threadIdx.x < sizeof(LinArgs) / 4)
+        reinterpret_cast<uint32_t*>(sm + L.args)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&args)[threadIdx.x];
     if (threadIdx.x < 16) xmax[threadIdx.x] = 0;
     if (threadIdx.x >= 64 && threadIdx.x < 64 + 128)
         reinterpret_cast<uint32_t*>(sm + L.ones)[threadIdx.x - 64] = FMT == MOE_NVFP4 ? 0x38383838u : 0x7F7F7F7Fu;
-    if (warp == 1) tmem_alloc(tmem_slot, a.tmem_cols);
+    if (warp == 1) tmem_alloc(tmem_slot, args.tmem_cols);
     fence_proxy_async_smem();   // the scale atom of ones
     tc_fence_before();
     __syncthreads();
@@ -331,33 +336,36 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         // digits first holds its elements as loaded; the same warp turns them into digits once
         // the tokens' largest elements are known.  Short loops, not unrolled copies: a CTA runs
         // this once, at the speed at which it can fetch the instructions
-        const int pw = warp - 1, items = Tp * KT;
+        const int pw = warp - 1, tp_inv = a.tp_inv, K = a.K;
+        const long long ldx = a.ldx;
+        const char* x = static_cast<const char*>(a.x);
         uint8_t* digits = sm + L.digits;                  // item (t, kt) at (kt * Tp + t) KiB
         constexpr int batch = XF32 ? 3 : 6;
-        for (int j0 = pw; j0 < items; j0 += batch * kLinPrepWarps) {
+        for (int j0 = pw; j0 < items; j0 += batch * nprep) {
             X8<XF32> v[batch];
 #pragma unroll
             for (int i = 0; i < batch; i++) {
-                const int j = j0 + i * kLinPrepWarps, kt = j / Tp;
-                v[i].load(a, j < items ? j - kt * Tp : T, k0 + kt * kLinKT + lane * 8);
+                const int j = j0 + i * nprep, kt = (j * tp_inv) >> 16;
+                const int t = j - kt * Tp, k = k0 + kt * kLinKT + lane * 8;
+                v[i].load(x + (t * ldx + k) * (XF32 ? 4 : 2), j < items && t < T && k < K);
             }
 #pragma unroll
             for (int i = 0; i < batch; i++) {
-                const int j = j0 + i * kLinPrepWarps;
+                const int j = j0 + i * nprep;
                 if (j >= items) break;
                 v[i].put(digits + j * 1024, lane);
                 uint32_t mx = 0;
 #pragma unroll
                 for (int e = 0; e < 8; e++) mx = max(mx, v[i].bits(e) & 0x7FFFFFFFu);
                 mx = __reduce_max_sync(0xffffffffu, mx);
-                if (lane == 0) atomicMax(&xmax[j % Tp], mx);
+                if (lane == 0) atomicMax(&xmax[j - ((j * tp_inv) >> 16) * Tp], mx);
             }
         }
         __syncwarp();
-        named_sync(1, kLinPrepWarps * 32);
+        named_sync(1, nprep * 32);
 #pragma unroll 1
-        for (int j = pw; j < items; j += kLinPrepWarps) {
-            const int t = j % Tp;
+        for (int j = pw; j < items; j += nprep) {
+            const int t = j - ((j * tp_inv) >> 16) * Tp;
             const uint32_t mx = xmax[t];
             // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
             const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
@@ -429,20 +437,28 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         uint4 q[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) q[i] = fetch();
-        digits_of_x();
+        if (nprep == 11) digits_of_x();
         const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
         int s = 0, ph = 0;
+#pragma unroll 1
         for (int it0 = 0; it0 < total; it0 += 4) {
+            // two stages at a time: rows to shared memory, then every warp takes all of them for
+            // its quarter of TMEM's lanes: lane l, column 4 i + j holds step i's scales of row
+            // l + 32 j.  Two buffers, one barrier a pair: a buffer's readers are past the next one
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (it0 + i < total) {
-                    // rows to shared memory, then every warp takes all of them for its quarter of
-                    // TMEM's lanes: lane l, column 4 i + j holds step i's scales of row l + 32 j.
-                    // Two buffers and one barrier a stage: a buffer's readers are past the next one
-                    uint8_t* buf = sm + L.scales + (i & 1) * 2048;
-                    *reinterpret_cast<uint4*>(buf + 16 * r) = q[i];
-                    __syncwarp();
-                    named_sync(2, 128);
+            for (int p = 0; p < 4; p += 2) {
+                const int n = min(2, total - it0 - p);
+                if (n <= 0) break;
+                uint8_t* buf = sm + L.scales + p * 2048;
+                *reinterpret_cast<uint4*>(buf + 16 * r) = q[p];
+                *reinterpret_cast<uint4*>(buf + 2048 + 16 * r) = q[p + 1];
+                q[p] = fetch();
+                q[p + 1] = fetch();
+                __syncwarp();
+                named_sync(2, 128);
+                const int s0 = s;
+#pragma unroll 1
+                for (int i = 0; i < n; i++, buf += 2048) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
@@ -457,12 +473,13 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                     __syncwarp();            // the lanes leave the wait one by one
                     tc_fence_after();
                     tmem_st_32x16(sf_base + 16 * s + quarter, w);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s]);
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
-                q[i] = fetch();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane < n) mbar_arrive(&full[s0 + lane < S ? s0 + lane : 0]);
+                __syncwarp();
             }
         }
     } else {
@@ -559,7 +576,7 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                 }
             }
             __syncwarp();
-            if (C > 1) cluster_arrive();
+            if (C > 1) cluster_arrive_relaxed();
         } else {
             const int tid = threadIdx.x - 64;
             const uint32_t peer_exe = map_rank(smem_addr(exe), lane < C ? lane : 0);
@@ -567,21 +584,29 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             const int quads = (T + 3) / 4;                    // a thread sums one row of four tokens
             const uint32_t in_bytes = 16 * C * NW * nown * quads;
             const int src_words = NW * R * ldt;
+            // (held in registers: the stores below would have them read again each time)
+            const int N = a.N, tiles = a.tiles, r_inv = a.r_inv;
+            const bool y_f32 = a.y_f32;
+            const long long ldy = a.ldy, ld_add = a.ld_add;
+            float* const yf = static_cast<float*>(a.y);
+            __nv_bfloat16* const yh = static_cast<__nv_bfloat16*>(a.y);
+            const float* const addf = static_cast<const float*>(a.add);
+            const __nv_bfloat16* const addh = static_cast<const __nv_bfloat16*>(a.add);
             if (C > 1) cluster_wait();
             int tc = 0;
-            for (int tile = cl; tile < a.tiles; tile += ncl, tc++) {
+            for (int tile = cl; tile < tiles; tile += ncl, tc++) {
                 const int b = tc & 1;
                 if (C > 1 && tid == 0) mbar_arrive_expect_tx(&exf[b], in_bytes);
                 if (!mbar_wait_cluster(&exf[b], (tc >> 1) & 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
                 __syncwarp();
-                if (C > 1 && tile + ncl >= a.tiles) cluster_arrive();   // no more access to peers from here
+                if (C > 1 && tile + ncl >= tiles) cluster_arrive_relaxed();   // no more access to peers from here
 #pragma unroll 1
                 for (int j = tid; j < quads * R; j += kLinSumThreads) {
-                    const int g = j / R, o = j - g * R, n = tile * TR + own0 + o;
-                    if (o >= nown || n >= a.N) continue;
+                    const int g = (j * r_inv) >> 16, o = j - g * R, n = tile * TR + own0 + o;
+                    if (o >= nown || n >= N) continue;
                     const float* in = exch + b * buf_words + o * ldt + 4 * g;
                     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
+#pragma unroll 4
                     for (int c = 0; c < C; c++, in += src_words) {
                         const float4 p = *reinterpret_cast<const float4*>(in);
                         y[0] += p.x; y[1] += p.y; y[2] += p.z; y[3] += p.w;
@@ -590,23 +615,28 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                             u[0] += q.x; u[1] += q.y; u[2] += q.z; u[3] += q.w;
                         }
                     }
-                    const int nt = min(4, T - 4 * g);
+                    if (GATED) {
 #pragma unroll
-                    for (int h = 0; h < 4; h++) {
-                        if (h >= nt) break;
-                        float v = y[h];
-                        const long long t = 4 * g + h;
-                        if (GATED) v = v / (1.0f + expf(-v)) * u[h];
-                        if (a.add)
-                            v += a.y_f32 ? static_cast<const float*>(a.add)[t * a.ld_add + n]
-                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.add)[t * a.ld_add + n]);
-                        if (a.y_f32) static_cast<float*>(a.y)[t * a.ldy + n] = v;
-                        else static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + n] = __float2bfloat16_rn(v);
+                        for (int h = 0; h < 4; h++) y[h] = y[h] / (1.0f + expf(-y[h])) * u[h];
                     }
+                    const int nt = min(4, T - 4 * g);
+                    const long long at = 4 * g * ldy + n;
+                    if (addf) {
+                        const long long from = 4 * g * ld_add + n;
+#pragma unroll
+                        for (int h = 0; h < 4; h++)
+                            if (h < nt) y[h] += y_f32 ? addf[from + h * ld_add] : __bfloat162float(addh[from + h * ld_add]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; h++)
+                        if (h < nt) {
+                            if (y_f32) yf[at + h * ldy] = y[h];
+                            else yh[at + h * ldy] = __float2bfloat16_rn(y[h]);
+                        }
                 }
                 __syncwarp();
                 // the buffer may be written again, if another tile will use it
-                if (tile + 2 * ncl < a.tiles) {
+                if (tile + 2 * ncl < tiles) {
                     if (C > 1) {
                         if (lane < C) mbar_arrive_cluster(peer_exe + 8 * b);
                     } else if (lane == 0) {
@@ -623,7 +653,7 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         __syncwarp();
         if (warp < 2 || warp >= 8) {
             cluster_wait();
-            cluster_arrive();
+            cluster_arrive_relaxed();
         }
         cluster_wait();
     }
@@ -706,6 +736,10 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     while (a.stages > 1 && LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024 > d.smem) a.stages--;
     const int smem = LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024;
     if (smem > d.smem) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
+    if (a.stages == 1 && total > 1) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
+    const int R = ((GATED ? 64 : 128) + a.C - 1) / a.C;
+    a.tp_inv = (65536 + Tp - 1) / Tp;
+    a.r_inv = (65536 + R - 1) / R;
     const int cols = 2 * 8 * Tp + 16 * a.stages + 4;
     a.tmem_cols = 32;
     while ((int)a.tmem_cols < cols) a.tmem_cols *= 2;
