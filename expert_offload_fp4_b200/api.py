@@ -149,20 +149,18 @@ def _rows(t, dtypes, rows, cols, what):
 def _call(name, tensors, stream, *args):
     """Library call on the device that holds all of `tensors`, on `stream` or that
     device's current stream."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: all tensors must be on one CUDA device")
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev or dev < 0:
             raise ValueError(f"{name}: all tensors must be on one CUDA device")
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
         raise ValueError(f"{name}: the stream belongs to another device than the tensors")
     else:
         handle = stream.cuda_stream
     fn = getattr(L.load(), name)
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == dev:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

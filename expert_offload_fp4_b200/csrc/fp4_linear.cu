@@ -34,6 +34,8 @@
 // All waits are bounded; a timeout sets bit 16 of *status and the CTA carries on.
 #include "tcgen05.cuh"
 
+#include <type_traits>
+
 namespace moe {
 
 int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
@@ -41,7 +43,7 @@ int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_
 
 constexpr int kLinThreads = 384;
 constexpr int kLinKT = 256;               // K elements of a stage (128 code bytes a row)
-constexpr int kLinMaxStages = 8;
+constexpr int kLinMaxStages = 5;
 constexpr int kLinMaxCluster = 8;
 constexpr int kLinSumThreads = 64;        // warps 2, 3
 
@@ -202,8 +204,9 @@ __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) 
 // X + 4 (8^8 - 1) / 7, whose plain octal digits are u_d + 4, as 8 selector nibbles, the
 // lowest digit in the lowest nibble.
 __device__ __forceinline__ uint32_t octal_nibbles(uint32_t u) {
-    const uint32_t w = (u & 0xFFFu) + (u & 0xFFF000u) * 16u;
-    return (w & 0x00070007u) + (w & 0x00380038u) * 2u + (w & 0x01C001C0u) * 4u + (w & 0x0E000E00u) * 8u;
+    const uint32_t w = u + (u & 0xFFF000u) * 15u;          // 12 bits to the upper half: x + h (2^4 - 1)
+    const uint32_t t = w + (w & 0x0FC00FC0u) * 3u;         // 6 bits to the next byte
+    return t + (t & 0x38383838u);                          // 3 bits to the next nibble
 }
 
 // 8 elements -> for each digit d the 4 bytes (8 codes) of B's row d.
@@ -232,17 +235,24 @@ __device__ __forceinline__ void digit_rows(const uint32_t (&X)[8], uint32_t (&ro
 
 // The scales of one row and stage: 16 bytes (NVFP4) or 8 (MXFP4, in x and y).  p: the
 // stage's first scale of the row, n: how many scales the row has from there (0 for
-// a row or stage outside).
-template <int FMT>
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide) {
+// a row or stage outside).  WIDE: rows are whole stages and aligned to them; else
+// bytes, two at a time where the address is even.
+template <int FMT, bool WIDE>
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n) {
     constexpr int per = FMT == MOE_NVFP4 ? 16 : 8;   // scales per stage
     uint32_t b[4] = {0, 0, 0, 0};
-    if (n >= per && wide) {
-        if constexpr (FMT == MOE_NVFP4) return __ldg(reinterpret_cast<const uint4*>(p));
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        b[0] = v.x;
-        b[1] = v.y;
-    } else if (n > 0) {
+    if (WIDE) {
+        if (n > 0) {
+            if constexpr (FMT == MOE_NVFP4) return __ldg(reinterpret_cast<const uint4*>(p));
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            return make_uint4(u.x, u.y, 0, 0);
+        }
+    } else if ((reinterpret_cast<uintptr_t>(p) & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < per / 2; i++)
+            if (2 * i + 1 < n) b[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << (16 * (i % 2));
+            else if (2 * i < n) b[i / 2] |= (uint32_t)__ldg(p + 2 * i) << (16 * (i % 2));
+    } else {
 #pragma unroll
         for (int i = 0; i < per; i++)
             if (i < n) b[i / 4] |= (uint32_t)__ldg(p + i) << (8 * (i % 4));
@@ -253,7 +263,7 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int n, bool wide)
 // ---------------------------------------------------------------- kernel
 
 template <int FMT, int GATED, int XF32>
-__global__ void __launch_bounds__(kLinThreads, 2)
+__global__ void __launch_bounds__(kLinThreads, 1)
 fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                   const __grid_constant__ LinArgs args) {
     extern __shared__ uint8_t smem_raw[];
@@ -331,74 +341,6 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     }
     pdl_wait();
 
-    auto digits_of_x = [&]() {
-        // digits of x: items are (token, 256 elements), 8 elements per lane.  An item's 1 KiB of
-        // digits first holds its elements as loaded; the same warp turns them into digits once
-        // the tokens' largest elements are known.  Short loops, not unrolled copies: a CTA runs
-        // this once, at the speed at which it can fetch the instructions
-        const int pw = warp - 1, tp_inv = a.tp_inv, K = a.K;
-        const long long ldx = a.ldx;
-        const char* x = static_cast<const char*>(a.x);
-        uint8_t* digits = sm + L.digits;                  // item (t, kt) at (kt * Tp + t) KiB
-        constexpr int batch = XF32 ? 3 : 6;
-        for (int j0 = pw; j0 < items; j0 += batch * nprep) {
-            X8<XF32> v[batch];
-#pragma unroll
-            for (int i = 0; i < batch; i++) {
-                const int j = j0 + i * nprep, kt = (j * tp_inv) >> 16;
-                const int t = j - kt * Tp, k = k0 + kt * kLinKT + lane * 8;
-                v[i].load(x + (t * ldx + k) * (XF32 ? 4 : 2), j < items && t < T && k < K);
-            }
-#pragma unroll
-            for (int i = 0; i < batch; i++) {
-                const int j = j0 + i * nprep;
-                if (j >= items) break;
-                v[i].put(digits + j * 1024, lane);
-                uint32_t mx = 0;
-#pragma unroll
-                for (int e = 0; e < 8; e++) mx = max(mx, v[i].bits(e) & 0x7FFFFFFFu);
-                mx = __reduce_max_sync(0xffffffffu, mx);
-                if (lane == 0) atomicMax(&xmax[j - ((j * tp_inv) >> 16) * Tp], mx);
-            }
-        }
-        __syncwarp();
-        named_sync(1, nprep * 32);
-#pragma unroll 1
-        for (int j = pw; j < items; j += nprep) {
-            const int t = j - ((j * tp_inv) >> 16) * Tp;
-            const uint32_t mx = xmax[t];
-            // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
-            const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
-            const bool finite = mx < 0x7F800000u;
-            const int up = 21 - E, h1 = up / 2, d1 = E / 2;
-            const float f1 = exp2i(h1), f2 = exp2i(up - h1);
-            uint8_t* dst = digits + j * 1024;
-            X8<XF32> v;
-            v.get(dst, lane);
-            // rounded by adding 1.5 2^23, whose bits X then counts from
-            uint32_t X[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                X[e] = __float_as_uint(fmaf(__uint_as_float(v.bits(e)) * f1, f2, 12582912.0f)) - 0x4B400000u + 0x924924u;
-            uint32_t row[8];
-            digit_rows(X, row);
-            __syncwarp();                                 // all lanes have their elements
-            // rows 8 t + d of the K-major operand, 128-byte swizzle: 16-byte chunk c of row d at c ^ d
-#pragma unroll
-            for (int d = 0; d < 8; d++)
-                *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = row[d];
-            if (j < Tp && lane == 0) {
-                xscale[t] = finite ? exp2i(d1) : __uint_as_float(0x7FC00000u);
-                xscale[16 + t] = exp2i(E - d1);
-            }
-        }
-        // (the MMA thread orders these stores before its reads: a proxy fence here would wait
-        // for warps 8-11's loads of scales)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bready);
-        __syncwarp();
-    };
-
     if (warp == 0) {
         if (lane == 0) {
             int s = 0, ph = 0;
@@ -414,7 +356,7 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                 }
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    } else {
         // block scales: thread r of warps 8-11 fetches row r's, a few stages ahead
         const int r = threadIdx.x & 127, which_r = GATED ? r >> 6 : 0;
         constexpr int BS = FMT == MOE_NVFP4 ? 16 : 32, per = kLinKT / BS;
@@ -423,10 +365,12 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         const int have = min(a.K - k0, a.Kc) / BS;       // scales of this CTA's part of a row
         const int total = ((a.tiles - cl + ncl - 1) / ncl) * KT;
         int f_it = 0, f_kt = 0, f_n = cl * TR + (GATED ? r & 63 : r);      // the next stage to fetch
-        auto fetch = [&]() -> uint4 {
-            const bool in = f_it < total && f_n < a.N;
+        const int N = a.N;
+        const bool wide = a.wide_scales;
+        auto fetch = [&](auto w) -> uint4 {
+            const bool in = f_it < total && f_n < N;
             const int o = f_kt * per;
-            const uint4 v = load_scales<FMT>(base + (in ? (size_t)f_n * pitch + o : 0), in ? have - o : 0, a.wide_scales);
+            const uint4 v = load_scales<FMT, decltype(w)::value>(base + (in ? (size_t)f_n * pitch + o : 0), in ? have - o : 0);
             f_it++;
             if (++f_kt == KT) {
                 f_kt = 0;
@@ -435,56 +379,78 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
             return v;
         };
         uint4 q[4];
+        if (warp >= 8 && wide) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) q[i] = fetch();
-        if (nprep == 11) digits_of_x();
-        const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
-        int s = 0, ph = 0;
-#pragma unroll 1
-        for (int it0 = 0; it0 < total; it0 += 4) {
-            // two stages at a time: rows to shared memory, then every warp takes all of them for
-            // its quarter of TMEM's lanes: lane l, column 4 i + j holds step i's scales of row
-            // l + 32 j.  Two buffers, one barrier a pair: a buffer's readers are past the next one
-#pragma unroll
-            for (int p = 0; p < 4; p += 2) {
-                const int n = min(2, total - it0 - p);
-                if (n <= 0) break;
-                uint8_t* buf = sm + L.scales + p * 2048;
-                *reinterpret_cast<uint4*>(buf + 16 * r) = q[p];
-                *reinterpret_cast<uint4*>(buf + 2048 + 16 * r) = q[p + 1];
-                q[p] = fetch();
-                q[p + 1] = fetch();
-                __syncwarp();
-                named_sync(2, 128);
-                const int s0 = s;
-#pragma unroll 1
-                for (int i = 0; i < n; i++, buf += 2048) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(buf + 16 * (lane + 32 * j));
-                        const bool nv = FMT == MOE_NVFP4;
-                        w[j] = nv ? u.x : u.x & 0xFFFFu;
-                        w[4 + j] = nv ? u.y : u.x >> 16;
-                        w[8 + j] = nv ? u.z : u.y & 0xFFFFu;
-                        w[12 + j] = nv ? u.w : u.y >> 16;
-                    }
-                    if (!mbar_wait(&empty[s], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
-                    __syncwarp();            // the lanes leave the wait one by one
-                    tc_fence_after();
-                    tmem_st_32x16(sf_base + 16 * s + quarter, w);
-                    if (++s == S) { s = 0; ph ^= 1; }
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane < n) mbar_arrive(&full[s0 + lane < S ? s0 + lane : 0]);
-                __syncwarp();
-            }
+            for (int i = 0; i < 4; i++) q[i] = fetch(std::true_type());
         }
-    } else {
-        digits_of_x();
-
+        __syncwarp();
+        if (warp < 8 || nprep == 11) {
+            // digits of x: items are (token, 256 elements), 8 elements per lane.  An item's 1 KiB of
+            // digits first holds its elements as loaded; the same warp turns them into digits once
+            // the tokens' largest elements are known.  Short loops, not unrolled copies: a CTA runs
+            // this once, at the speed at which it can fetch the instructions
+            const int pw = warp - 1, tp_inv = a.tp_inv, K = a.K;
+            const long long ldx = a.ldx;
+            const char* x = static_cast<const char*>(a.x);
+            uint8_t* digits = sm + L.digits;                  // item (t, kt) at (kt * Tp + t) KiB
+            constexpr int batch = XF32 ? 2 : 4;
+            for (int j0 = pw; j0 < items; j0 += batch * nprep) {
+                X8<XF32> v[batch];
+#pragma unroll
+                for (int i = 0; i < batch; i++) {
+                    const int j = j0 + i * nprep, kt = (j * tp_inv) >> 16;
+                    const int t = j - kt * Tp, k = k0 + kt * kLinKT + lane * 8;
+                    v[i].load(x + (t * ldx + k) * (XF32 ? 4 : 2), j < items && t < T && k < K);
+                }
+#pragma unroll
+                for (int i = 0; i < batch; i++) {
+                    const int j = j0 + i * nprep;
+                    if (j >= items) break;
+                    v[i].put(digits + j * 1024, lane);
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) mx = max(mx, v[i].bits(e) & 0x7FFFFFFFu);
+                    mx = __reduce_max_sync(0xffffffffu, mx);
+                    if (lane == 0) atomicMax(&xmax[j - ((j * tp_inv) >> 16) * Tp], mx);
+                }
+            }
+            __syncwarp();
+            named_sync(1, nprep * 32);
+#pragma unroll 1
+            for (int j = pw; j < items; j += nprep) {
+                const int t = j - ((j * tp_inv) >> 16) * Tp;
+                const uint32_t mx = xmax[t];
+                // E: exponent of the largest element (subnormals as they are); 2^(21 - E) in two factors
+                const int E = mx == 0 ? 0 : mx < 0x00800000u ? -118 - __clz(mx) : (int)(mx >> 23) - 127;
+                const bool finite = mx < 0x7F800000u;
+                const int up = 21 - E, h1 = up / 2, d1 = E / 2;
+                const float f1 = exp2i(h1), f2 = exp2i(up - h1);
+                uint8_t* dst = digits + j * 1024;
+                X8<XF32> v;
+                v.get(dst, lane);
+                // rounded by adding 1.5 2^23, whose bits X then counts from
+                uint32_t X[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    X[e] = __float_as_uint(fmaf(__uint_as_float(v.bits(e)) * f1, f2, 12582912.0f)) - 0x4B400000u + 0x924924u;
+                uint32_t row[8];
+                digit_rows(X, row);
+                __syncwarp();                                 // all lanes have their elements
+                // rows 8 t + d of the K-major operand, 128-byte swizzle: 16-byte chunk c of row d at c ^ d
+#pragma unroll
+                for (int d = 0; d < 8; d++)
+                    *reinterpret_cast<uint32_t*>(dst + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = row[d];
+                if (j < Tp && lane == 0) {
+                    xscale[t] = finite ? exp2i(d1) : __uint_as_float(0x7FC00000u);
+                    xscale[16 + t] = exp2i(E - d1);
+                }
+            }
+            // (the MMA thread orders these stores before its reads: a proxy fence here would wait
+            // for warps 8-11's loads of scales)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bready);
+            __syncwarp();
+        }
         const int R = (TR + C - 1) / C;                   // output rows per owner
         constexpr int NW = GATED ? 2 : 1;
         const int ldt = lin_row_words(Tp);
@@ -492,7 +458,68 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
         float* exch = reinterpret_cast<float*>(sm + L.exch);
         __syncwarp();
 
-        if (warp == 1) {
+        if (warp >= 8) {
+            const uint32_t quarter = (uint32_t)(32 * (warp - 8)) << 16;
+            int s = 0, ph = 0;
+            auto stages = [&](auto w) {
+                using W = decltype(w);
+#pragma unroll 1
+                for (int it0 = 0; it0 < total; it0 += 4) {
+                    // two stages at a time: rows to shared memory, then every warp takes all of them for
+                    // its quarter of TMEM's lanes: lane l, column 4 i + j holds step i's scales of row
+                    // l + 32 j.  Two buffers, one barrier a pair: a buffer's readers are past the next one
+#pragma unroll
+                    for (int p = 0; p < 4; p += 2) {
+                        const int n = min(2, total - it0 - p);
+                        if (n <= 0) break;
+                        uint8_t* buf = sm + L.scales + p * 2048;
+                        if (!W::value) {
+                            q[p] = fetch(w);
+                            q[p + 1] = fetch(w);
+                        }
+                        *reinterpret_cast<uint4*>(buf + 16 * r) = q[p];
+                        *reinterpret_cast<uint4*>(buf + 2048 + 16 * r) = q[p + 1];
+                        if (W::value) {          // four stages ahead
+                            q[p] = fetch(w);
+                            q[p + 1] = fetch(w);
+                        }
+                        __syncwarp();
+                        named_sync(2, 128);
+                        // everything that can wait first, then the loads and stores of both stages in a row
+                        const int s0 = s, s1 = s + 1 == S ? 0 : s + 1;
+                        if (!mbar_wait(&empty[s0], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                        if (++s == S) { s = 0; ph ^= 1; }
+                        if (n == 2) {
+                            if (!mbar_wait(&empty[s1], ph ^ 1, a.limit_ns) && lane == 0) atomicOr(a.status, 1 << 16);
+                            if (++s == S) { s = 0; ph ^= 1; }
+                        }
+                        __syncwarp();                // the lanes leave the waits one by one
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < n; i++) {
+                            uint32_t c[16];
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const uint4 u = *reinterpret_cast<const uint4*>(buf + 2048 * i + 16 * (lane + 32 * j));
+                                const bool nv = FMT == MOE_NVFP4;
+                                c[j] = nv ? u.x : u.x & 0xFFFFu;
+                                c[4 + j] = nv ? u.y : u.x >> 16;
+                                c[8 + j] = nv ? u.z : u.y & 0xFFFFu;
+                                c[12 + j] = nv ? u.w : u.y >> 16;
+                            }
+                            tmem_st_32x16(sf_base + 16 * (i == 0 ? s0 : s1) + quarter, c);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane < n) mbar_arrive(&full[lane == 0 ? s0 : s1]);
+                        __syncwarp();
+                    }
+                }
+            };
+            if (wide) stages(std::true_type());
+            else stages(std::false_type());
+        } else if (warp == 1) {
             if (lane == 0) {
                 if (!mbar_wait(bready, 0, a.limit_ns)) atomicOr(a.status, 1 << 16);
                 fence_proxy_async_smem();
@@ -713,19 +740,20 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
             active[C] = n < 1 ? 1 : n;
         }
     }
-    // Cluster size: the fewest stages on the busiest CTA, small clusters first.  The digits
-    // of x take 4 Tp Kc bytes; with at most 64 KiB of them 8 stages fit beside them.
+    // Cluster size: the least of, in twentieths of a stage's 0.4 us, the stages of the busiest
+    // CTA, the conversion of its part of x (0.15 a KiB of digits) and the exchange of each tile
+    // (0.5).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9.
+    // At most 128 KiB of digits, so that four stages fit beside them
     int bestC = 0;
     long long best = 0;
-    for (int cap = 64 * 1024; cap <= 128 * 1024 && !bestC; cap *= 2)
-        for (int C = 1; C <= kLinMaxCluster && C <= KTall; C++) {
-            const int kt = (KTall + C - 1) / C;
-            if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
-            if (4 * Tp * kt * kLinKT > cap) continue;
-            const int ncl = std::min(a.tiles, active[C]);
-            const long long cost = (long long)((a.tiles + ncl - 1) / ncl) * kt;
-            if (!bestC || cost < best) { best = cost; bestC = C; }
-        }
+    for (int C = 1; C <= kLinMaxCluster && C <= KTall; C++) {
+        const int kt = (KTall + C - 1) / C;
+        if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
+        if (4 * Tp * kt * kLinKT > 128 * 1024) continue;
+        const int ncl = std::min(a.tiles, active[C]), rounds = (a.tiles + ncl - 1) / ncl;
+        const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 10 * rounds;
+        if (!bestC || cost < best) { best = cost; bestC = C; }
+    }
     if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens (K * T, T rounded up to even, at most 262144)");
     a.C = bestC;
     const int kt = (KTall + a.C - 1) / a.C;
