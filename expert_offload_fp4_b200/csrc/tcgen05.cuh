@@ -91,6 +91,15 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// D[tmem] (+)= A[smem] x B[smem]^T, kind::f16 (both operands bf16, as idesc says).
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
 // 32 rows x 16 bytes of shared memory (one scale-factor atom: row r of the atom
 // holds the 4+4+4+4 scales of rows r, r+32, r+64, r+96) to TMEM lanes 0-31,
 // replicated to all four lane quarters, 4 columns.

@@ -249,8 +249,8 @@ int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias
  * scores sum to 0 the renormalised weights are 0.  idx is always within [0, E).
  * x [T, H] and W_r [E, H] bf16, 16-byte aligned rows (H % 8 == 0); outputs idx
  * [T, k] int32 and w [T, k] fp32 in rank order.  workspace: device scratch of
- * moe_route_grouped_workspace_bytes(T, E) bytes, 16-byte aligned, zeroed before its
- * first use (every call leaves its counters zero); calls that may overlap, and
+ * moe_route_grouped_workspace_bytes(T, E) bytes, 256-byte aligned, zeroed before its
+ * first use (every call leaves its counters, the first 256 bytes, zero); calls that may overlap, and
  * captured graphs that may be replayed at the same time, need one each.  E <= 1024.
  * Errors: MOE_EINVAL. */
 size_t moe_route_grouped_workspace_bytes(int T, int E);
