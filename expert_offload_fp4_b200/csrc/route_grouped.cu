@@ -6,11 +6,10 @@
 // that CTA) makes the choice, one warp a token.
 //
 // Many tokens (a prompt): fp64 would take 100 times the tensor cores' time.  A tcgen05
-// GEMM gives the logits in fp32 together with |x_t| and |W_e|, from which a bound
-// delta = kGemmError |x| |W| on a logit's error follows; the choice then computes a
-// logit again in fp64, from x and W_r, only where a decision hangs on less than that
-// bound allows (a few tokens in a hundred, a few experts each).  So both ways choose
-// the same experts.
+// GEMM gives the logits in fp32 together with |x_t| and |W_e|, from which a bound on
+// a logit's error follows; the choice then computes a logit again in fp64, from x and
+// W_r, only where a decision hangs on less than that bound allows (a few tokens in a
+// hundred, a few experts each).  So both ways choose the same experts.
 #include "tcgen05.cuh"
 #include "route_select.cuh"
 
@@ -38,29 +37,36 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 }
 
 // One token's choice by a warp from exact logits l64(e); rounded: they are more than fp32 holds.
-template <int VPL, class L64>
+template <class L64>
 __device__ __forceinline__ void choose_row(L64 l64, bool rounded, uint8_t* scratch, const RouteChoice& p, int lane,
                                            int32_t* idx_out, float* w_out) {
-    float lf[VPL], mx;
+    const RouteScratch s(scratch, p.E);
     unsigned big = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane + 32 * i;
-        lf[i] = e < p.E ? (float)l64(e) : 0.0f;
-        big = max(big, __float_as_uint(lf[i]) & 0x7FFFFFFFu);
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32) {
+        const double l = l64(e);
+        s.fill(e, l, (float)l, p.bias);
+        big = max(big, __float_as_uint((float)l) & 0x7FFFFFFFu);
     }
+    __syncwarp();
     // (an infinite or NaN one makes delta so too, and route_fast gives up)
     const float delta = rounded ? __uint_as_float(__reduce_max_sync(0xffffffffu, big)) * 0x1p-23f : 0.0f;
     int my_e;
-    if (route_fast<VPL>(lf, p, delta, lane, scratch, mx, my_e)) {
-        route_fast_weights<VPL>(lf, p, mx, lane, my_e, l64, idx_out, w_out);
+    float mx;
+    bool masked;
+    RouteClose close;
+    const RouteStatus st = route_fast(s, p, delta, lane, mx, my_e, masked, close);
+    __syncwarp();
+    if (st == kRouteOpen) {
+        route_choose_exact(s, p, lane, idx_out, w_out);
         return;
     }
-    const RouteScratch s(scratch, p.E);
-    __syncwarp();
-    for (int e = lane; e < p.E; e += 32) s.l[e] = l64(e);
-    __syncwarp();
-    route_choose_exact<VPL>(s, p, lane, idx_out, w_out);
+    if (st == kRouteClose) {
+        const double inv = !p.sigmoid && p.bias ? route_softmax_inv(s.l, p.E, mx, lane) : 1.0;
+        my_e = route_settle(s, p, close, mx, inv, lane);
+        masked = route_bias_masks(p, my_e);
+    }
+    route_weights(s, p, mx, lane, my_e, masked, idx_out, w_out);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -84,65 +90,74 @@ __device__ __forceinline__ double warp_sum_tokens(double (&v)[TT], int lane) {
     return v[0];
 }
 
-template <int TT, int VPL>
+template <int TT>
 __global__ void __launch_bounds__(kChooseWarps * 32)
 grouped_small_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int T, int H, RouteChoice p,
                      int32_t* __restrict__ idx, float* __restrict__ wout, double* __restrict__ logits,
                      unsigned int* __restrict__ tile_cnt) {
     extern __shared__ __align__(16) uint8_t sm_raw[];
-    __shared__ double part[kChooseWarps][TT];
+    __shared__ double part[kChooseWarps][2 * TT];
     __shared__ int s_last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = blockIdx.y * TT, nt = min(TT, T - t0);
-    const int e = blockIdx.x * 2 + (warp >> 2);
+    const int e0 = blockIdx.x * 2, e1 = min(e0 + 1, p.E - 1);
     const int nch = H / 8;
     pdl_trigger();
-    if (e < p.E)
-        for (int c = quarter * 32 + lane; c < nch; c += 128) prefetch_l2(wr + size_t(e) * H + c * 8);
+    for (int c = threadIdx.x; c < nch; c += kChooseWarps * 32) {
+        prefetch_l2(wr + size_t(e0) * H + c * 8);
+        prefetch_l2(wr + size_t(e1) * H + c * 8);
+    }
     pdl_wait();
-    double acc[TT];
+    double acc[2 * TT];
 #pragma unroll
-    for (int t = 0; t < TT; t++) acc[t] = 0.0;
-    if (e < p.E) {
-        const uint4* wrow = reinterpret_cast<const uint4*>(wr + size_t(e) * H);
-        const uint4* xrow = reinterpret_cast<const uint4*>(x + size_t(t0) * H);
-        constexpr int U = TT >= 8 ? 1 : 2;   // chunks whose loads are in flight together
+    for (int t = 0; t < 2 * TT; t++) acc[t] = 0.0;
+    const uint4* w0 = reinterpret_cast<const uint4*>(wr + size_t(e0) * H);
+    const uint4* w1 = reinterpret_cast<const uint4*>(wr + size_t(e1) * H);
+    const uint4* xrow = reinterpret_cast<const uint4*>(x + size_t(t0) * H);
+    constexpr int U = TT >= 8 ? 1 : 2;   // chunks whose loads are in flight together
 #pragma unroll 1
-        for (int c0 = quarter * 32 + lane; c0 < nch; c0 += 128 * U) {
-            uint4 wq[U], xq[U][TT];
+    for (int c0 = threadIdx.x; c0 < nch; c0 += kChooseWarps * 32 * U) {
+        uint4 wq[U][2], xq[U][TT];
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int c = c0 + 128 * u;
-                wq[u] = c < nch ? __ldg(wrow + c) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U; u++) {
+            const int c = c0 + kChooseWarps * 32 * u;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            wq[u][0] = c < nch ? __ldg(w0 + c) : zero;
+            wq[u][1] = c < nch ? __ldg(w1 + c) : zero;
 #pragma unroll
-                for (int t = 0; t < TT; t++)
-                    xq[u][t] = c < nch && t < nt ? xrow[size_t(t) * nch + c] : make_uint4(0, 0, 0, 0);
+            for (int t = 0; t < TT; t++) xq[u][t] = c < nch && t < nt ? xrow[size_t(t) * nch + c] : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            double wd[2][8];
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+                float wf[8];
+                unpack8(wq[u][a], wf);
+#pragma unroll
+                for (int r = 0; r < 8; r++) wd[a][r] = wf[r];
             }
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                float wf[8];
-                unpack8(wq[u], wf);
-                double wd[8];
+            for (int t = 0; t < TT; t++) {
+                float xf[8];
+                unpack8(xq[u][t], xf);
 #pragma unroll
-                for (int r = 0; r < 8; r++) wd[r] = wf[r];
-#pragma unroll
-                for (int t = 0; t < TT; t++) {
-                    float xf[8];
-                    unpack8(xq[u][t], xf);
-#pragma unroll
-                    for (int r = 0; r < 8; r++) acc[t] = fma((double)xf[r], wd[r], acc[t]);
+                for (int r = 0; r < 8; r++) {
+                    const double xd = xf[r];
+                    acc[t] = fma(xd, wd[0][r], acc[t]);
+                    acc[TT + t] = fma(xd, wd[1][r], acc[TT + t]);
                 }
             }
         }
     }
-    const double v = warp_sum_tokens<TT>(acc, lane);
-    if (lane % (32 / TT) == 0) part[warp][lane / (32 / TT)] = v;
+    const double v = warp_sum_tokens<2 * TT>(acc, lane);
+    if (lane % (16 / TT) == 0) part[warp][lane / (16 / TT)] = v;
     __syncthreads();
     if (threadIdx.x < 2 * TT) {
-        const int h = threadIdx.x / TT, t = threadIdx.x % TT, ee = blockIdx.x * 2 + h;
-        if (ee < p.E && t < nt)
-            logits[size_t(t0 + t) * p.E + ee] =
-                (part[4 * h][t] + part[4 * h + 1][t]) + (part[4 * h + 2][t] + part[4 * h + 3][t]);
+        const int h = threadIdx.x / TT, t = threadIdx.x % TT, ee = e0 + h;
+        double sum = 0.0;
+        for (int w = 0; w < kChooseWarps; w++) sum += part[w][threadIdx.x];
+        if (ee < p.E && t < nt) logits[size_t(t0 + t) * p.E + ee] = sum;
         __threadfence();
     }
     __syncthreads();
@@ -156,70 +171,110 @@ grouped_small_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict_
     if (threadIdx.x == 0) tile_cnt[blockIdx.y] = 0;
     if (warp >= nt) return;
     const double* row = logits + size_t(t0 + warp) * p.E;
-    choose_row<VPL>([&](int e) { return __ldcg(row + e); }, true, sm_raw + warp * RouteScratch::bytes(p.E), p, lane,
+    choose_row([&](int e) { return __ldcg(row + e); }, true, sm_raw + warp * RouteScratch::bytes(p.E), p, lane,
                     idx + size_t(t0 + warp) * p.k, wout + size_t(t0 + warp) * p.k);
 }
 
 // ---------------------------------------------------------------- many tokens: logits
 
 constexpr int kRgStages = 4;
-constexpr int kRgThreads = 512;
+constexpr int kRgThreads = 384;
 constexpr int kRgMaxSplit = 16;
 constexpr int kRgMaxN = 256;             // experts per CTA
 constexpr int kRgTargetCtas = 148;
+constexpr int kRgChunk = 2;              // stages (64 elements each) the tensor core sums by itself
 
-// A logit's error over |x_t| |W_e|, per element of a CTA's part of H: every MMA step of 16
-// elements may cut the accumulator, whose size |x| |W| bounds, by one unit in its 24th bit,
-// and as much again in lining up its products: 2^-23 a step, 2^-27 an element.  Measured: 2^-29
-// where all products are positive, 2^-33 for normal ones.
-constexpr double kGemmError = 0x1p-27;
+// Error of the tensor core's sums over |x_t| |W_e|: every MMA step of 16 elements may cut the
+// accumulator by one unit in its 24th bit and as much again in lining up its products, 2^-23 of
+// its size, which |x| |W| of the chunk bounds; 8 steps a chunk, and the chunks' bounds add up to
+// 2^-20 |x| |W|.  (Measured per step: 2^-25.6 where all products are positive.)  The chunks are
+// added in fp32 registers: 2^-24 of the largest sum each.
+constexpr double kGemmError = 0x1p-20;
 
 struct RouteGemmArgs {
     int T, H, E, Ep;          // Ep: row length of the partial logits
     int n_tiles, N, split, Kc;
     float* part;              // [split][T][Ep]
     float* xn;                // [split][T] sums of squares of x
+    float* xm;                // [split][n_tiles][T] largest sum of a row
     float* wn;                // [E] sums of squares of W_r
     const uint16_t* wr;
     unsigned long long limit_ns;
 };
 
-// One CTA: 128 tokens x N experts over Kc of H.  Warp 0 loads (TMA, 128-byte swizzle),
-// warp 1 issues the MMAs, warps 8-15 sum the squares of a share of W_r, warps 4-7 those of
-// the x rows as they pass through shared memory, then drain the accumulator.  Waits are
-// bounded; where one gives up, the bound on the errors becomes NaN.
+// 32 lanes x 16 consecutive fp32 columns; complete after tcgen05.wait::ld.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15},"
+        " [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// One CTA: 128 tokens x N experts over Kc of H.  Warp 0 loads (TMA, 128-byte swizzle), warp 1
+// issues the MMAs into two accumulators in turn, a chunk of K each; warps 4-11 add the chunks up
+// in registers (a row and 128 experts a thread), after the sums of squares of a share of W_r;
+// warps 2-3 sum the squares of the x rows as they pass through shared memory (two rows a
+// thread), apart from the others because a stage is free only when they have read it.  Waits
+// are bounded; where one gives up, the bound on the errors becomes NaN.
 __global__ void __launch_bounds__(kRgThreads, 1)
 route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                   const RouteGemmArgs g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kRgStages], empty[kRgStages], accf;
+    __shared__ __align__(8) uint64_t full[kRgStages], empty[kRgStages], accf[2], acce[2];
     __shared__ uint32_t tmem_slot;
+    __shared__ unsigned s_max[128];      // largest |sum| per row (float bits)
+    __shared__ float s_sq[128];          // sums of squares of the rows
     __shared__ int s_bad;                // a wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b_bytes = g.N * 128, stage = 16384 + b_bytes;
     const int rank = blockIdx.x % g.split, tile = blockIdx.x / g.split;
     const int nt = tile % g.n_tiles, mt = tile / g.n_tiles;
-    const int k0 = rank * g.Kc, KT = (min(g.H - k0, g.Kc) + 63) / 64;
-    const uint32_t cols = g.N <= 32 ? 32 : g.N <= 64 ? 64 : g.N <= 128 ? 128 : 256;
+    const int k0 = rank * g.Kc, KT = (min(g.H - k0, g.Kc) + 63) / 64, chunks = (KT + kRgChunk - 1) / kRgChunk;
+    const uint32_t cols = g.N <= 16 ? 32 : g.N <= 32 ? 64 : g.N <= 64 ? 128 : g.N <= 128 ? 256 : 512;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRgStages; s++) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1 + 4);
+            mbar_init(&empty[s], 1 + 2);
         }
-        mbar_init(&accf, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&acce[i], 8);
+        }
         s_bad = 0;
         fence_mbar_init();
         prefetch_tmap(&map_x);
         prefetch_tmap(&map_w);
     }
+    if (threadIdx.x < 128) s_max[threadIdx.x] = 0;
     if (warp == 1) tmem_alloc(&tmem_slot, cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t acc = tmem_slot;
+    const uint32_t tbase = tmem_slot;
     pdl_trigger();
     pdl_wait();
+
+    // sums of squares of W_r: experts dealt out to the warps w of n a CTA
+    auto w_norms = [&](int w, int n) {
+        for (int e = blockIdx.x * n + w; e < g.E; e += gridDim.x * n) {
+            const uint4* row = reinterpret_cast<const uint4*>(g.wr + size_t(e) * g.H);
+            float sum = 0.0f;
+#pragma unroll 8
+            for (int c = lane; c < g.H / 8; c += 32) {
+                float v[8];
+                unpack8(__ldg(row + c), v);
+#pragma unroll
+                for (int r = 0; r < 8; r++) sum = fmaf(v[r], v[r], sum);
+            }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) g.wn[e] = sum;
+        }
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -238,241 +293,299 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             // D fp32, A and B bf16, K-major, M = 128
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(g.N >> 3) << 17) | (8u << 24);
             int s = 0, ph = 0;
-            for (int kt = 0; kt < KT; kt++) {
-                if (!mbar_wait(&full[s], ph, g.limit_ns)) s_bad = 1;
-                tc_fence_after();
-                const uint64_t ad = smem_desc(sm + s * stage, 16, 1024, 2), bd = smem_desc(sm + s * stage + 16384, 16, 1024, 2);
+            for (int j = 0; j < chunks; j++) {
+                if (!mbar_wait(&acce[j & 1], ((j >> 1) & 1) ^ 1, g.limit_ns)) s_bad = 1;
+                const uint32_t acc = tbase + (j & 1) * g.N;
+                for (int kt = j * kRgChunk; kt < min(KT, (j + 1) * kRgChunk); kt++) {
+                    if (!mbar_wait(&full[s], ph, g.limit_ns)) s_bad = 1;
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc(sm + s * stage, 16, 1024, 2), bd = smem_desc(sm + s * stage + 16384, 16, 1024, 2);
 #pragma unroll
-                for (int i = 0; i < 4; i++)   // K = 16 elements = 32 bytes per MMA
-                    mma_bf16(acc, ad + 2 * i, bd + 2 * i, idesc, (kt > 0 || i > 0) ? 1u : 0u);
-                tc_commit(&empty[s]);
-                if (++s == kRgStages) { s = 0; ph ^= 1; }
+                    for (int i = 0; i < 4; i++)   // K = 16 elements = 32 bytes per MMA
+                        mma_bf16(acc, ad + 2 * i, bd + 2 * i, idesc, (kt > j * kRgChunk || i > 0) ? 1u : 0u);
+                    tc_commit(&empty[s]);
+                    if (++s == kRgStages) { s = 0; ph ^= 1; }
+                }
+                tc_commit(&accf[j & 1]);
             }
-            tc_commit(&accf);
         }
         __syncwarp();
-    } else if (warp >= 8) {
-        for (int e = blockIdx.x * 8 + warp - 8; e < g.E; e += gridDim.x * 8) {
-            const uint4* row = reinterpret_cast<const uint4*>(g.wr + size_t(e) * g.H);
-            float sum = 0.0f;
-#pragma unroll 8
-            for (int c = lane; c < g.H / 8; c += 32) {
-                float v[8];
-                unpack8(__ldg(row + c), v);
-#pragma unroll
-                for (int r = 0; r < 8; r++) sum = fmaf(v[r], v[r], sum);
-            }
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) g.wn[e] = sum;
-        }
-    } else if (warp >= 4) {
-        const int r = threadIdx.x - 128, t = mt * 128 + r;
-        float sum = 0.0f;
+    } else if (warp < 4) {
+        const int r = threadIdx.x - 64;
+        float sq[2] = {0.0f, 0.0f};
         int s = 0, ph = 0;
         for (int kt = 0; kt < KT; kt++) {
             if (!mbar_wait(&full[s], ph, g.limit_ns)) s_bad = 1;
-            const uint4* row = reinterpret_cast<const uint4*>(sm + s * stage + r * 128);
+            __syncwarp();
             if (nt == 0) {
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    float v[8];
-                    unpack8(row[(c + r) & 7], v);   // a quarter warp's rows in different banks
+                for (int h = 0; h < 2; h++) {
+                    const uint4* row = reinterpret_cast<const uint4*>(sm + s * stage + (r + 64 * h) * 128);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) sum = fmaf(v[i], v[i], sum);
+                    for (int c = 0; c < 8; c++) {
+                        float v[8];
+                        unpack8(row[(c + r) & 7], v);   // a quarter warp's rows in different banks
+#pragma unroll
+                        for (int i = 0; i < 8; i++) sq[h] = fmaf(v[i], v[i], sq[h]);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == kRgStages) { s = 0; ph ^= 1; }
         }
-        if (!mbar_wait(&accf, 0, g.limit_ns)) s_bad = 1;
+        s_sq[r] = sq[0];
+        s_sq[r + 64] = sq[1];
         __syncwarp();
-        // (a bound of NaN has the choice compute the token's logits in fp64)
-        if (t < g.T && (nt == 0 || s_bad)) g.xn[(size_t)rank * g.T + t] = s_bad ? __uint_as_float(0x7FC00000u) : sum;
-        tc_fence_after();
-        float* dst = g.part + ((size_t)rank * g.T + t) * g.Ep + nt * kRgMaxN;
-        const int width = min(g.N, g.Ep - nt * kRgMaxN);
-        for (int c = 0; c < width; c += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32(acc + ((uint32_t)(32 * (warp - 4)) << 16) + c, v);
-            if (t < g.T) {
+        named_sync(1, 320);
+    } else {
+        const int r = 32 * (warp & 3) + lane, t = mt * 128 + r, half = (warp - 4) >> 2;
+        const int width = min(g.N, g.Ep - nt * kRgMaxN) - half * 128;   // columns of this thread
+        w_norms(warp - 4, 8);
+        __syncwarp();
+        float sum[8][16], top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)   // whole 32-byte sectors
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + i), "r"(v[i]),
-                                 "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]),
-                                 "r"(v[i + 7]) : "memory");
+        for (int b = 0; b < 8; b++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) sum[b][i] = 0.0f;
+        for (int j = 0; j < chunks; j++) {
+            if (!mbar_wait(&accf[j & 1], (j >> 1) & 1, g.limit_ns)) s_bad = 1;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t acc = tbase + (j & 1) * g.N + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
+#pragma unroll
+            for (int b = 0; b < 8; b++) {
+                if (16 * b >= width) break;
+                uint32_t v[16];
+                tmem_ld_32x16(acc + 16 * b, v);
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    sum[b][i] += __uint_as_float(v[i]);
+                    top = fmaxf(top, fabsf(sum[b][i]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acce[j & 1]);
+        }
+        if (width > 0) atomicMax(&s_max[r], __float_as_uint(top));
+        __syncwarp();
+        named_sync(1, 320);
+        if (half == 0 && t < g.T) {
+            // (a bound of NaN has the choice compute the token's logits in fp64)
+            if (nt == 0) g.xn[(size_t)rank * g.T + t] = s_sq[r];
+            g.xm[((size_t)rank * g.n_tiles + nt) * g.T + t] = s_bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(s_max[r]);
+        }
+        if (t < g.T) {
+            float* dst = g.part + ((size_t)rank * g.T + t) * g.Ep + nt * kRgMaxN + half * 128;
+#pragma unroll
+            for (int b = 0; b < 8; b++) {
+                if (16 * b >= width) break;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)   // whole 32-byte sectors
+                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * b + i),
+                                 "f"(sum[b][i]), "f"(sum[b][i + 1]), "f"(sum[b][i + 2]), "f"(sum[b][i + 3]),
+                                 "f"(sum[b][i + 4]), "f"(sum[b][i + 5]), "f"(sum[b][i + 6]), "f"(sum[b][i + 7]) : "memory");
             }
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(acc, cols);
+        tmem_dealloc(tbase, cols);
     }
 }
 
 // ---------------------------------------------------------------- many tokens: choice
 
-// fp64 dot products of one x row with rows e[0 .. NE) of W_r by a warp.
-template <int NE>
-__device__ __forceinline__ void exact_logits(const uint16_t* x, const uint16_t* wr, int H, const int (&e)[NE], int lane,
-                                             double (&out)[NE]) {
-    double acc[NE];
+// What a warp's token still needs.
+enum ChooseMode {
+    kDone,
+    kRanks,      // exact logits of a few experts, then the order of their ranks
+    kAttempt,    // exact logits of the marked experts, then another route_attempt
+    kAll         // every logit in fp64
+};
+
+struct ChooseShared {
+    int n[kChooseWarps];                      // wanted logits per token
+    int want[kChooseWarps][32];               // their experts (n > 32: all)
+    double got[kChooseWarps][32];             // their values
+    double part[2][kChooseWarps][4];          // the warps' parts of four dot products
+};
+
+// The wanted logits of the CTA's tokens in fp64, by all warps: each takes an eighth of H,
+// four dot products at a time.  Values go to got, or to the token's scratch where all are wanted.
+__device__ __forceinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, const uint16_t* x, const uint16_t* wr, int H, int E,
+                                             int t0, int warp, int lane) {
+    int total = 0;
+    for (int h = 0; h < kChooseWarps; h++) total += sh.n[h];
+    for (int j0 = 0, buf = 0; j0 < total; j0 += 4, buf ^= 1) {
+        const uint4 *xr[4], *wrow[4];
 #pragma unroll
-    for (int a = 0; a < NE; a++) acc[a] = 0.0;
-    constexpr int U = 4;                 // chunks in flight
-#pragma unroll 1
-    for (int c0 = lane; c0 < H / 8; c0 += 32 * U) {
-        uint4 xq[U], wq[U][NE];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int c = c0 + 32 * u;
-            const bool in = c < H / 8;
-            xq[u] = in ? __ldg(reinterpret_cast<const uint4*>(x) + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int a = 0; a < NE; a++)
-                wq[u][a] = in ? __ldg(reinterpret_cast<const uint4*>(wr + size_t(e[a]) * H) + c) : make_uint4(0, 0, 0, 0);
+        for (int a = 0; a < 4; a++) {
+            int h = 0, j = min(j0 + a, total - 1);
+            while (j >= sh.n[h]) j -= sh.n[h++];
+            const int e = sh.n[h] > 32 ? j : sh.want[h][j];
+            xr[a] = reinterpret_cast<const uint4*>(x + size_t(t0 + h) * H);
+            wrow[a] = reinterpret_cast<const uint4*>(wr + size_t(e) * H);
         }
+        double acc[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+        for (int c = warp * 32 + lane; c < H / 8; c += 32 * kChooseWarps) {
+            uint4 xq[4], wq[4];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            float xf[8];
-            unpack8(xq[u], xf);
-            double xd[8];
+            for (int a = 0; a < 4; a++) {
+                xq[a] = __ldg(xr[a] + c);
+                wq[a] = __ldg(wrow[a] + c);
+            }
 #pragma unroll
-            for (int r = 0; r < 8; r++) xd[r] = xf[r];
+            for (int a = 0; a < 4; a++) {
+                float xf[8], wf[8];
+                unpack8(xq[a], xf);
+                unpack8(wq[a], wf);
 #pragma unroll
-            for (int a = 0; a < NE; a++) {
-                float wf[8];
-                unpack8(wq[u][a], wf);
-#pragma unroll
-                for (int r = 0; r < 8; r++) acc[a] = fma(xd[r], (double)wf[r], acc[a]);
+                for (int r = 0; r < 8; r++) acc[a] = fma((double)xf[r], (double)wf[r], acc[a]);
             }
         }
+        const double v = warp_sum_tokens<4>(acc, lane);
+        if (lane % 8 == 0) sh.part[buf][warp][lane / 8] = v;
+        __syncthreads();
+        if (threadIdx.x < 4 && j0 + (int)threadIdx.x < total) {
+            double sum = 0.0;
+            for (int w = 0; w < kChooseWarps; w++) sum += sh.part[buf][w][threadIdx.x];
+            int h = 0, j = j0 + threadIdx.x;
+            while (j >= sh.n[h]) j -= sh.n[h++];
+            if (sh.n[h] > 32) RouteScratch(scratch + h * RouteScratch::bytes(E), E).l[j] = sum;
+            else sh.got[h][j] = sum;
+        }
     }
-#pragma unroll
-    for (int a = 0; a < NE; a++) out[a] = warp_sum(acc[a]);
+    __syncthreads();
 }
 
-// One warp per token.  Logits that have to be known exactly are computed by all warps of
-// the CTA together, whichever token they belong to.
-template <int VPL>
+// One warp per token.
 __global__ void __launch_bounds__(kChooseWarps * 32)
 route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, RouteGemmArgs g, RouteChoice p,
                          int32_t* __restrict__ idx, float* __restrict__ wout) {
     extern __shared__ __align__(16) uint8_t sm_raw[];
-    __shared__ unsigned s_mark[kChooseWarps][32];   // bit i of word j: expert j + 32 i is wanted
+    __shared__ ChooseShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kChooseWarps + warp;
+    const int t0 = blockIdx.x * kChooseWarps, t = t0 + warp;
     const RouteScratch s(sm_raw + warp * RouteScratch::bytes(p.E), p.E);
+    int32_t* idx_t = idx + size_t(t) * p.k;
+    float* w_t = wout + size_t(t) * p.k;
     pdl_trigger();
     pdl_wait();
+    int mode = kDone, my_e = 0;
     unsigned mark = 0;
-    bool open = false, all = false;      // not chosen yet; every logit is wanted
+    float delta = 0.0f, mx = 0.0f;
+    RouteClose close;
     RouteSoftmax sm;
     double eta = 0.0;
+    auto attempt = [&]() {
+        if (!route_attempt(s, p, eta, lane, mark, my_e)) {
+            mode = __reduce_add_sync(0xffffffffu, __popc(mark)) > 32 ? kAll : kAttempt;
+            return;
+        }
+        route_weights(s, p, sm.mx, lane, my_e, route_bias_masks(p, my_e), idx_t, w_t);
+        mode = kDone;
+    };
     if (t < g.T) {
-        float lf[VPL], mx, wmax = 0.0f, xn = 0.0f;
+        float wmax = 0.0f, xn = 0.0f, xm = 0.0f;
+        for (int e = 4 * lane; e < p.E; e += 128) {
+            const float* col = g.part + (size_t)t * g.Ep + e;      // (rows are padded to 32)
+            float4 l = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int c = 0; c < g.split; c++) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(col + (size_t)c * g.T * g.Ep));
+                l.x += v.x; l.y += v.y; l.z += v.z; l.w += v.w;
+            }
+            const float v[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-        for (int i = 0; i < VPL; i++) lf[i] = 0.0f;
-        for (int c = 0; c < g.split; c++) {
-            const float* row = g.part + ((size_t)c * g.T + t) * g.Ep + lane;
-            xn += __ldg(g.xn + (size_t)c * g.T + t);
+            for (int i = 0; i < 4; i++)
+                if (e + i < p.E) s.fill(e + i, v[i], v[i], p.bias);
+        }
+        for (int c = lane; c < g.split; c += 32) xn += __ldg(g.xn + (size_t)c * g.T + t);
+        // (the sum over the tiles of experts is more than their largest: a NaN stays)
+        for (int c = lane; c < g.split * g.n_tiles; c += 32) xm += __ldg(g.xm + (size_t)c * g.T + t);
 #pragma unroll
-            for (int i = 0; i < VPL; i++)
-                if (lane + 32 * i < p.E) lf[i] += __ldg(row + 32 * i);
+        for (int off = 16; off >= 1; off >>= 1) {
+            xn += __shfl_xor_sync(0xffffffffu, xn, off);
+            xm += __shfl_xor_sync(0xffffffffu, xm, off);
         }
         for (int e = lane; e < p.E; e += 32) {
             const float w2 = __ldg(g.wn + e);
-            wmax = !(w2 <= wmax) ? w2 : wmax;   // a NaN stays
+            wmax = !(w2 <= wmax) ? w2 : wmax;
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
             const float o = __shfl_xor_sync(0xffffffffu, wmax, off);
             wmax = !(o <= wmax) ? o : wmax;
         }
-        // (the parts' sum in fp32 adds one rounding each)
-        const float delta = (float)(kGemmError * (g.Kc + 8 * g.split) * 1.001 * sqrt((double)xn * (double)wmax));
-        int my_e;
-        open = true;
+        delta = (float)(1.001 * (kGemmError * sqrt((double)xn * (double)wmax) +
+                                 0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
         if (!(delta <= 0.05f)) {
-            all = true;
-        } else if (route_fast<VPL>(lf, p, delta, lane, s.l, mx, my_e)) {
-            const float* sl = reinterpret_cast<const float*>(s.l);
-            route_fast_weights<VPL>(lf, p, mx, lane, my_e, [&](int e) { return (double)sl[e]; }, idx + size_t(t) * p.k,
-                                    wout + size_t(t) * p.k);
-            open = false;
-        } else if (!p.sigmoid && p.bias) {
-            all = true;                  // the denominator hangs on every logit
+            mode = kAll;
         } else {
+            bool masked;
+            const RouteStatus st = route_fast(s, p, delta, lane, mx, my_e, masked, close);
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < VPL; i++)
-                if (lane + 32 * i < p.E) s.l[lane + 32 * i] = lf[i];
-            __syncwarp();
-            eta = route_first_values<VPL>(s, p, delta, lane, sm);
-            if (route_attempt<VPL>(s, p, eta, lane, mark, my_e)) {
-                route_weights(p, sm.mx, lane, my_e, s.l[my_e], [&]() { return route_softmax_inv(s.l, p.E, sm.mx, lane); },
-                              idx + size_t(t) * p.k, wout + size_t(t) * p.k);
-                open = false;
-                mark = 0;
+            if (st == kRouteCertain) {
+                route_weights(s, p, mx, lane, my_e, masked, idx_t, w_t);
+            } else if (!p.sigmoid && p.bias) {
+                mode = kAll;                 // the denominator hangs on every logit
+            } else if (st == kRouteClose) {
+                mode = kRanks;
+            } else {
+                eta = route_first_values(s, p, delta, lane, sm);
+                attempt();
             }
         }
-        if (all)
-#pragma unroll
-            for (int i = 0; i < VPL; i++)
-                if (lane + 32 * i < p.E) mark |= 1u << i;
     }
-    while (__syncthreads_or(open)) {
-        s_mark[warp][lane] = open ? mark : 0;
-        __syncthreads();
-        int seen = 0;                    // wanted logits so far: the CTA's warps take them in turn, two at a time
-        for (int h = 0; h < kChooseWarps; h++) {
-            const unsigned word = s_mark[h][lane];
-            int before = __popc(word);   // inclusive prefix sum over the lanes
+    while (__syncthreads_or(mode != kDone)) {
+        // publish what is wanted
+        int n = mode == kAll ? p.E : 0, at = 0;      // at: this lane's first in the list
+        if (mode == kAll && n <= 32) {
+            if (lane < n) sh.want[warp][lane] = lane;
+        } else if (mode == kRanks) {
+            const unsigned wants = __ballot_sync(0xffffffffu, close.want);
+            n = __popc(wants);
+            at = __popc(wants & ((1u << lane) - 1));
+            if (close.want) sh.want[warp][at] = close.e;
+        } else if (mode == kAttempt) {
+            at = __popc(mark);
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane >= off) before += o;
+                const int o = __shfl_up_sync(0xffffffffu, at, off);
+                if (lane >= off) at += o;
             }
-            const int n = __shfl_sync(0xffffffffu, before, 31);
-            before -= __popc(word);
-            const int th = blockIdx.x * kChooseWarps + h;
-            const RouteScratch sh(sm_raw + h * RouteScratch::bytes(p.E), p.E);
-            for (int j = 0; j < n; j += 2) {
-                if (((seen + j) / 2) % kChooseWarps != warp) continue;
-                int e[2];
-#pragma unroll
-                for (int a = 0; a < 2; a++) {
-                    const int m = min(j + a, n - 1);
-                    const int src = 31 - __clz(__ballot_sync(0xffffffffu, before <= m && word != 0));
-                    unsigned w = __shfl_sync(0xffffffffu, word, src);
-                    for (int skip = m - __shfl_sync(0xffffffffu, before, src); skip > 0; skip--) w &= w - 1;
-                    e[a] = src + 32 * (__ffs(w) - 1);
-                }
-                double v[2];
-                exact_logits<2>(x + size_t(th) * g.H, wr, g.H, e, lane, v);
-                if (lane == 0) {
-                    sh.l[e[0]] = v[0];
-                    sh.l[e[1]] = v[1];
-                }
-            }
-            seen += (n + 1) / 2 * 2;
+            n = __shfl_sync(0xffffffffu, at, 31);
+            at -= __popc(mark);
+            int j = at;
+            for (unsigned m = mark; m; m &= m - 1) sh.want[warp][j++] = lane + 32 * (__ffs(m) - 1);
         }
+        if (lane == 0) sh.n[warp] = n;
         __syncthreads();
-        if (open && all) {
-            route_choose_exact<VPL>(s, p, lane, idx + size_t(t) * p.k, wout + size_t(t) * p.k);
-            open = false;
-        } else if (open) {
-            for (; mark; mark &= mark - 1) route_make_exact(s, p, sm, lane + 32 * (__ffs(mark) - 1));
+        exact_logits(sh, sm_raw, x, wr, g.H, p.E, t0, warp, lane);
+        if (mode == kAll) {
+            if (n <= 32 && lane < n) s.l[lane] = sh.got[warp][lane];
             __syncwarp();
-            int my_e;
-            if (route_attempt<VPL>(s, p, eta, lane, mark, my_e)) {
-                route_weights(p, sm.mx, lane, my_e, s.l[my_e], [&]() { return route_softmax_inv(s.l, p.E, sm.mx, lane); },
-                              idx + size_t(t) * p.k, wout + size_t(t) * p.k);
-                open = false;
+            route_choose_exact(s, p, lane, idx_t, w_t);
+            mode = kDone;
+        } else if (mode == kRanks) {
+            if (close.want) s.l[close.e] = sh.got[warp][at];
+            __syncwarp();
+            my_e = route_settle(s, p, close, mx, 1.0, lane);
+            route_weights(s, p, mx, lane, my_e, route_bias_masks(p, my_e), idx_t, w_t);
+            mode = kDone;
+        } else if (mode == kAttempt) {
+            int j = at;
+            for (unsigned m = mark; m; m &= m - 1) {
+                const int e = lane + 32 * (__ffs(m) - 1);
+                s.l[e] = sh.got[warp][j++];
+                route_make_exact(s, p, sm, e);
             }
+            __syncwarp();
+            attempt();
         }
     }
 }
@@ -480,7 +593,6 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
 // ---------------------------------------------------------------- given logits
 
 // One warp per token; logits fp32 or bf16 with row stride ld.
-template <int VPL>
 __global__ void __launch_bounds__(kChooseWarps * 32)
 route_select_kernel(const void* __restrict__ logits, int is_bf16, long long ld, int T, RouteChoice p,
                     int32_t* __restrict__ idx, float* __restrict__ wout) {
@@ -492,7 +604,7 @@ route_select_kernel(const void* __restrict__ logits, int is_bf16, long long ld, 
     if (t >= T) return;
     const uint16_t* lh = reinterpret_cast<const uint16_t*>(logits) + t * ld;
     const float* lf = reinterpret_cast<const float*>(logits) + t * ld;
-    choose_row<VPL>([&](int e) { return (double)(is_bf16 ? __uint_as_float((uint32_t)lh[e] << 16) : lf[e]); }, false,
+    choose_row([&](int e) { return (double)(is_bf16 ? __uint_as_float((uint32_t)lh[e] << 16) : lf[e]); }, false,
                     sm_raw + warp * RouteScratch::bytes(p.E), p, lane, idx + size_t(t) * p.k, wout + size_t(t) * p.k);
 }
 
@@ -546,9 +658,9 @@ struct RouteCall {
     cudaStream_t s;
 };
 
-template <int TT, int VPL>
+template <int TT>
 static cudaError_t launch_small(const RouteCall& r) {
-    auto kern = grouped_small_kernel<TT, VPL>;
+    auto kern = grouped_small_kernel<TT>;
     static bool done[64] = {};
     cudaError_t e = raise_smem(kern, (int)(kSmallTile * RouteScratch::bytes(kMaxE)), done);
     if (e != cudaSuccess) return e;
@@ -557,7 +669,6 @@ static cudaError_t launch_small(const RouteCall& r) {
                       (double*)(r.ws + kCounterBytes), (unsigned int*)r.ws);
 }
 
-template <int VPL>
 static int launch_large(const RouteCall& r) {
     const int E = r.p.E;
     RouteGemmArgs g{};
@@ -574,6 +685,8 @@ static int launch_large(const RouteCall& r) {
     at += up256(size_t(g.split) * r.T * g.Ep * 4);
     g.xn = (float*)at;
     at += up256(size_t(g.split) * r.T * 4);
+    g.xm = (float*)at;
+    at += up256(size_t(g.split) * g.n_tiles * r.T * 4);
     g.wn = (float*)at;
     g.wr = r.wr;
     g.limit_ns = 2000000000ull;
@@ -586,25 +699,23 @@ static int launch_large(const RouteCall& r) {
     MOE_CUDA_TRY(raise_smem(route_gemm_kernel, kRgStages * (16384 + kRgMaxN * 128) + 1024, gdone));
     const dim3 grid(((r.T + 127) / 128) * g.n_tiles * g.split);
     MOE_CUDA_TRY(launch_pdl(route_gemm_kernel, grid, dim3(kRgThreads), smem, r.s, mx, mw, g));
-    auto kern = route_gemm_choose_kernel<VPL>;
+    auto kern = route_gemm_choose_kernel;
     MOE_CUDA_TRY(raise_smem(kern, (int)(kChooseWarps * RouteScratch::bytes(kMaxE)), cdone));
     MOE_CUDA_TRY(launch_pdl(kern, dim3((r.T + kChooseWarps - 1) / kChooseWarps), dim3(kChooseWarps * 32),
                             kChooseWarps * RouteScratch::bytes(E), r.s, r.x, r.wr, g, r.p, r.idx, r.w));
     return MOE_OK;
 }
 
-template <int VPL>
 static int launch_grouped(const RouteCall& r) {
-    if (r.T > kSmallT) return launch_large<VPL>(r);
-    const cudaError_t e = r.T == 1 ? launch_small<1, VPL>(r) : r.T == 2 ? launch_small<2, VPL>(r)
-                          : r.T <= 4 ? launch_small<4, VPL>(r) : launch_small<8, VPL>(r);
+    if (r.T > kSmallT) return launch_large(r);
+    const cudaError_t e = r.T == 1 ? launch_small<1>(r) : r.T == 2 ? launch_small<2>(r)
+                          : r.T <= 4 ? launch_small<4>(r) : launch_small<8>(r);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped router launch");
 }
 
-template <int VPL>
 static int launch_select(const void* logits, int bf16, long long ld, int T, const RouteChoice& p, int32_t* idx, float* w,
                          cudaStream_t s) {
-    auto kern = route_select_kernel<VPL>;
+    auto kern = route_select_kernel;
     static bool done[64] = {};
     MOE_CUDA_TRY(raise_smem(kern, (int)(kChooseWarps * RouteScratch::bytes(kMaxE)), done));
     MOE_CUDA_TRY(launch_pdl(kern, dim3((T + kChooseWarps - 1) / kChooseWarps), dim3(kChooseWarps * 32),
@@ -620,7 +731,8 @@ extern "C" size_t moe_route_grouped_workspace_bytes(int T, int E) {
     if (T <= 0 || E <= 0 || E > kMaxE) return 0;
     if (T <= kSmallT) return kCounterBytes + up256(size_t(T) * E * sizeof(double));
     const size_t split = route_split(T, E), Ep = (E + 31) / 32 * 32;
-    return kCounterBytes + up256(split * T * Ep * 4) + up256(split * T * 4) + up256(size_t(E) * 4);
+    const size_t tiles = (E + kRgMaxN - 1) / kRgMaxN;
+    return kCounterBytes + up256(split * T * Ep * 4) + up256(split * T * 4) + up256(split * tiles * T * 4) + up256(size_t(E) * 4);
 }
 
 extern "C" int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H, int E,
@@ -637,8 +749,7 @@ extern "C" int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const 
         return fail(MOE_EINVAL, "grouped route: workspace missing or smaller than moe_route_grouped_workspace_bytes");
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_EINVAL, "grouped route: workspace must be 256-byte aligned");
     const RouteCall r{(const uint16_t*)x_bf16, (const uint16_t*)wr_bf16, T, H, p, idx, w, (char*)workspace, (cudaStream_t)stream};
-    // registers per lane that hold the E selection values
-    return E <= 128 ? launch_grouped<4>(r) : E <= 256 ? launch_grouped<8>(r) : launch_grouped<32>(r);
+    return launch_grouped(r);
 }
 
 extern "C" int moe_route_select(const void* logits, int type, long long ld, const float* bias, int T, int E,
@@ -651,9 +762,5 @@ extern "C" int moe_route_select(const void* logits, int type, long long ld, cons
     if (ld < E && T > 1) return fail(MOE_EINVAL, "route select: row stride smaller than E");
     if (reinterpret_cast<uintptr_t>(logits) & (type == MOE_BF16 ? 1 : 3))
         return fail(MOE_EINVAL, "route select: logits not aligned to their type");
-    const int bf16 = type == MOE_BF16;
-    cudaStream_t s = (cudaStream_t)stream;
-    return E <= 128 ? launch_select<4>(logits, bf16, ld, T, p, idx, w, s)
-         : E <= 256 ? launch_select<8>(logits, bf16, ld, T, p, idx, w, s)
-                    : launch_select<32>(logits, bf16, ld, T, p, idx, w, s);
+    return launch_select(logits, type == MOE_BF16, ld, T, p, idx, w, (cudaStream_t)stream);
 }

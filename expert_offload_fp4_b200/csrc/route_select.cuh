@@ -58,15 +58,24 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// A warp's scratch for one token, in shared memory: E of each.
+// A warp's scratch for one token, in shared memory.  fill() the logits and biases of all
+// experts before the choice; the fp64 way reuses the fp32 arrays.
 struct RouteScratch {
     double* l;                   // logits
-    unsigned long long* key;     // order_key of the selection values
-    unsigned char* exact;        // 1: that value is the fp64 one
-    static __host__ __device__ size_t bytes(int E) { return (size_t(17) * E + 15) / 16 * 16; }
+    float *l32, *bias;           // in fp32, and the bias (0 without one)
+    unsigned* key32;             // order_key32 of the selection values
+    unsigned long long* key;     // order_key of the selection values (overlays l32 and key32)
+    unsigned char* exact;        // 1: that value is the fp64 one (overlays bias)
+    static __host__ __device__ size_t bytes(int E) { return (size_t(20) * E + 15) / 16 * 16; }
     __device__ RouteScratch(void* p, int E)
-        : l(static_cast<double*>(p)), key(reinterpret_cast<unsigned long long*>(l + E)),
-          exact(reinterpret_cast<unsigned char*>(key + E)) {}
+        : l(static_cast<double*>(p)), l32(reinterpret_cast<float*>(l + E)), bias(l32 + 2 * E),
+          key32(reinterpret_cast<unsigned*>(l32 + E)), key(reinterpret_cast<unsigned long long*>(l32)),
+          exact(reinterpret_cast<unsigned char*>(bias)) {}
+    __device__ __forceinline__ void fill(int e, double v, float v32, const float* b) const {
+        l[e] = v;
+        l32[e] = v32;
+        bias[e] = b ? __ldg(b + e) : 0.0f;
+    }
 };
 
 // ---------------------------------------------------------------- fp32 first
@@ -78,26 +87,81 @@ __device__ __forceinline__ unsigned order_key32(float c) {
 __device__ __forceinline__ float key32_value(unsigned q) { return __uint_as_float((q >> 31) ? (q & 0x7fffffffu) : ~q); }
 constexpr unsigned kMaskedKey32 = 0x007fffffu;   // order_key32(-inf)
 
-// The choice from fp32 logits lf[i] of expert lane + 32 i, each within delta of its logit;
-// returns whether it is certain, with my_e the expert of rank `lane`, mx the largest logit.
-// sc: scratch of 8 E bytes.
-template <int VPL>
-__device__ __forceinline__ bool route_fast(const float (&lf)[VPL], const RouteChoice& p, float delta, int lane, void* sc,
-                                           float& mx, int& my_e) {
-    float* sl = static_cast<float*>(sc);
-    unsigned* sk = reinterpret_cast<unsigned*>(sl + p.E);
-    bool odd = false;                      // NaN and infinities are left to the 64-bit way
+enum RouteStatus {
+    kRouteCertain,   // the choice stands
+    kRouteClose,     // the groups stand, but some ranks are too close to call: see RouteClose
+    kRouteOpen       // left to the 64-bit way
+};
+
+// The ranks and the experts just below them, one a lane (lanes >= n: none).
+struct RouteClose {
+    int n = 0, e = 0;
+    float c = 0.0f;      // selection value (by_logit: the logit)
+    bool want = false;   // it has to be known exactly
+    bool by_logit = false;
+};
+
+// A warp's best expert by 32-bit keys, taken out of sk; each lane keeps the best of its experts
+// lane, lane + 32, ...  (Here and below short loops over shared memory, not unrolled copies over
+// registers: a decode step runs this once, at the speed at which it can fetch the instructions;
+// 2.0 us against 5.7 for 256 experts.)
+struct RouteTop32 {
+    unsigned* sk;
+    int E, lane, e = 0, e2 = 0;
+    unsigned q = 0, q2 = 0;      // the lane's best and second
+    bool two = false;            // the second is known
+    __device__ __forceinline__ RouteTop32(unsigned* sk_, int E_, int lane_) : sk(sk_), E(E_), lane(lane_) { rescan(); }
+    __device__ __forceinline__ void rescan() {
+        q = q2 = 0;
+#pragma unroll 4
+        for (int i = lane; i < E; i += 32) {
+            const unsigned v = sk[i];
+            if (v > q) {      // ascending e: ties keep the lower
+                q2 = q;
+                e2 = e;
+                q = v;
+                e = i;
+            } else if (v > q2) {
+                q2 = v;
+                e2 = i;
+            }
+        }
+        two = true;
+    }
+    __device__ __forceinline__ unsigned best() const { return __reduce_max_sync(0xffffffffu, q); }
+    // the lowest expert whose key is `top`, which no longer takes part
+    __device__ __forceinline__ int take(unsigned top) {
+        const int win = (int)__reduce_min_sync(0xffffffffu, q == top ? unsigned(e) : 0xffffffffu);
+        if (q == top && e == win) {
+            sk[win] = 0;
+            if (two) {
+                q = q2;
+                e = e2;
+                two = false;
+            } else {
+                rescan();
+            }
+        }
+        return win;
+    }
+};
+
+// The choice from the fp32 logits, each within delta of its logit.  If it is certain, my_e is
+// the expert of rank `lane` (masked: chosen for want of others); mx: the largest logit.
+__device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const RouteChoice& p, float delta, int lane, float& mx,
+                                                  int& my_e, bool& masked, RouteClose& close_out) {
+    const float* sl = s.l32;
+    unsigned* sk = s.key32;
+    bool odd = delta > 0.05f;              // also NaN and infinities: left to the 64-bit way
     unsigned m = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane + 32 * i;
-        if (e >= p.E) continue;
-        m = max(m, order_key32(lf[i]));
-        odd |= !(lf[i] < INFINITY);
-        sl[e] = lf[i];
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32) {
+        const float l = sl[e];
+        m = max(m, order_key32(l));
+        odd |= !(l < INFINITY);
     }
     mx = key32_value(__reduce_max_sync(0xffffffffu, m));
-    if (mx == -INFINITY || delta > 0.05f) odd = true;
+    odd |= mx == -INFINITY;
     // Without a bias scores order as the logits do: no score is needed for the choice, as long
     // as fp64 scores differ wherever fp32 logits do
     const bool grouped = p.topk_group < p.n_group;
@@ -105,36 +169,28 @@ __device__ __forceinline__ bool route_fast(const float (&lf)[VPL], const RouteCh
     float inv = 1.0f;
     if (!p.sigmoid && p.bias) {
         float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; i++)
-            if (lane + 32 * i < p.E) sum += __expf(lf[i] - mx);
+        for (int e = lane; e < p.E; e += 32) sum += __expf(sl[e] - mx);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         inv = __fdividef(1.0f, sum);
     }
-    unsigned q[VPL];
     float cmax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane + 32 * i;
-        q[i] = 0;
-        if (e >= p.E) continue;
-        float c = lf[i], b = 0.0f;
+#pragma unroll 2
+    for (int e = lane; e < p.E; e += 32) {
+        const float l = sl[e];
+        float c = l;
         if (!by_logit) {
-            c = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-lf[i])) : __expf(lf[i] - mx) * inv;
-            if (p.bias) {
-                b = __ldg(p.bias + e);
-                c += b;
-            }
-            const bool masked = lf[i] == -INFINITY || b == -INFINITY;
-            if (masked) c = -INFINITY;
-            else odd |= !(fabsf(c) < 1e30f);
-            if (!masked) cmax = fmaxf(cmax, fabsf(c));
+            const float b = s.bias[e];
+            const float x = __expf(p.sigmoid ? -l : l - mx);
+            c = (p.sigmoid ? __fdividef(1.0f, 1.0f + x) : x * inv) + b;
+            const bool out = l == -INFINITY || b == -INFINITY;
+            odd |= !out && !(fabsf(c) < 1e30f);
+            cmax = fmaxf(cmax, out ? 0.0f : fabsf(c));
+            if (out) c = -INFINITY;
         }
-        q[i] = order_key32(c);
-        if (grouped) sk[e] = q[i];
+        sk[e] = order_key32(c);
     }
-    if (__any_sync(0xffffffffu, odd)) return false;
+    if (__any_sync(0xffffffffu, odd)) return kRouteOpen;
     // The error of a value: of the logit (|ds/dl| <= 1/4 for a sigmoid), and of the score in
     // fp32 (__expf, sum and quotient: below 2^-21 of the largest score, 2^-18 with a softmax's
     // denominator), and of adding the bias
@@ -153,12 +209,14 @@ __device__ __forceinline__ bool route_fast(const float (&lf)[VPL], const RouteCh
         const int sh = 31 - __clz(32 / p.n_group), per = 1 << sh;
         const int g = lane >> sh, r = lane & (per - 1);
         unsigned a = 0, b = 0;
-        if (g < p.n_group)
-            for (int e = g * gs + r; e < (g + 1) * gs; e += per) {
-                const unsigned v = sk[e];
+        if (g < p.n_group) {
+#pragma unroll 2
+            for (int e = r; e < gs; e += per) {
+                const unsigned v = sk[g * gs + e];
                 b = max(b, min(a, v));
                 a = max(a, v);
             }
+        }
         for (int off = per / 2; off >= 1; off >>= 1) {
             const unsigned oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
             b = max(max(b, ob), min(a, oa));
@@ -169,6 +227,7 @@ __device__ __forceinline__ bool route_fast(const float (&lf)[VPL], const RouteCh
         if (p.group_top == 2 && b > kMaskedKey32) G += key32_value(b);
         unsigned left = leader ? order_key32(G) : 0;
         unsigned kept = 0, lowest = 0;   // kept: bit of the leader lane
+#pragma unroll 1
         for (int j = 0; j < p.topk_group; j++) {
             lowest = __reduce_max_sync(0xffffffffu, left);
             const unsigned win = __ballot_sync(0xffffffffu, left == lowest);
@@ -177,51 +236,65 @@ __device__ __forceinline__ bool route_fast(const float (&lf)[VPL], const RouteCh
         }
         const unsigned next = __reduce_max_sync(0xffffffffu, left);
         // (equal exact logits are a tie, which the lower group has won)
-        if (eta > 0.0f && key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta) return false;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const int e = lane + 32 * i;
-            if (e < p.E && !((kept >> ((e / gs) << sh)) & 1u)) q[i] = 0;
-        }
+        if (eta > 0.0f && key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta) return kRouteOpen;
+        // take the other groups out
+        if (g < p.n_group && !((kept >> (g << sh)) & 1u))
+            for (int e = r; e < gs; e += per) sk[g * gs + e] = 0;
+        __syncwarp();
     }
-    // ranks 0 .. k: the last only to compare with
-    unsigned my_q = 0, after = 0;
+    RouteTop32 top(sk, p.E, lane);
+    unsigned my_q = 0;
     my_e = 0;
-    for (int j = 0; j <= p.k; j++) {
-        unsigned best = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) best = max(best, q[i]);
-        const unsigned top = __reduce_max_sync(0xffffffffu, best);
-        if (j == p.k) {
-            after = top;
-            break;
-        }
-        int at = VPL;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; i--) at = q[i] == top ? i : at;
-        const unsigned win = __reduce_min_sync(0xffffffffu, at < VPL ? unsigned(lane + 32 * at) : 0xffffffffu);
+#pragma unroll 1
+    for (int j = 0; j < p.k; j++) {
+        const unsigned q = top.best();
+        const int win = top.take(q);
         if (lane == j) {
-            my_e = (int)win;
-            my_q = top;
+            my_e = win;
+            my_q = q;
         }
-        const int wi = (win & 31) == lane ? int(win >> 5) : -1;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) q[i] = i == wi ? 0 : q[i];
     }
+    masked = my_q == kMaskedKey32;
+    const unsigned after = top.best();
+    const float last = key32_value(__shfl_sync(0xffffffffu, my_q, p.k - 1));
     // (scores this far down may be equal in fp64)
-    if (by_logit && key32_value(__shfl_sync(0xffffffffu, my_q, p.k - 1)) < (p.sigmoid ? -600.0f : mx - 600.0f)) return false;
-    if (eta == 0.0f) return true;
+    if (by_logit && last < (p.sigmoid ? -600.0f : mx - 600.0f)) return kRouteOpen;
+    if (eta == 0.0f) return kRouteCertain;
     unsigned below = __shfl_down_sync(0xffffffffu, my_q, 1);
     int below_e = __shfl_down_sync(0xffffffffu, my_e, 1);
     if (lane == p.k - 1) {
         below = after;
         below_e = -1;
     }
-    bool close = false;
-    if (lane < p.k && below != 0 && key32_value(my_q) - key32_value(below) <= 2 * eta)
-        // equal exact logits without a bias have equal scores: a tie
-        close = !(delta == 0.0f && !p.bias && my_q == below && below_e >= 0 && sl[my_e] == sl[below_e]);
-    return !__any_sync(0xffffffffu, close);
+    const bool close = lane < p.k && below != 0 && key32_value(my_q) - key32_value(below) <= 2 * eta;
+    // (equal exact logits without a bias have equal scores: a tie)
+    const bool tie = close && delta == 0.0f && !p.bias && my_q == below && below_e >= 0 && sl[my_e] == sl[below_e];
+    if (!__any_sync(0xffffffffu, close && !tie)) return kRouteCertain;
+    const unsigned links = __ballot_sync(0xffffffffu, close);   // bit i: ranks i and i + 1 may change places
+    // every rank of a link, and what may come up from below the last rank
+    int n = p.k;
+    if ((links >> (p.k - 1)) & 1u) {
+        const unsigned near = order_key32(last - 2 * eta);
+        for (int i = 0; i < p.E; i += 32) {
+            const unsigned v = i + lane < p.E ? sk[i + lane] : 0;
+            unsigned h = __ballot_sync(0xffffffffu, v != 0 && v >= near);
+            for (; h; h &= h - 1, n++) {       // one a lane, from lane k on
+                const int src = __ffs(h) - 1;
+                const unsigned q = __shfl_sync(0xffffffffu, v, src);
+                if (lane == n) {
+                    my_e = i + src;
+                    my_q = q;
+                }
+            }
+        }
+        if (n > 32) return kRouteOpen;
+    }
+    close_out.n = n;
+    close_out.e = my_e;
+    close_out.c = key32_value(my_q);
+    close_out.by_logit = by_logit;
+    close_out.want = lane < p.k ? ((links >> lane) & 1u) || (lane > 0 && ((links >> (lane - 1)) & 1u)) : lane < n;
+    return kRouteClose;
 }
 
 // ---------------------------------------------------------------- fp64 where it is close
@@ -249,29 +322,21 @@ __device__ __noinline__ double route_score64(double l, int sigmoid, double mx) {
 // One attempt at the choice from s.key.  Returns false, with the bits of `mark` set for
 // this lane's experts (bit i: expert lane + 32 i) that have to be known exactly first,
 // or true with my_e the expert of rank `lane`.
-template <int VPL>
-__device__ __forceinline__ bool route_attempt(const RouteScratch& s, const RouteChoice& p, double eta, int lane,
-                                              unsigned& mark, int& my_e) {
-    unsigned long long q[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane + 32 * i;
-        q[i] = e < p.E ? s.key[e] : 0;
-    }
+__device__ __noinline__ bool route_attempt(const RouteScratch s, const RouteChoice& p, double eta, int lane, unsigned& mark,
+                                           int& my_e) {
     mark = 0;
+    const int gs = p.E / p.n_group;
+    unsigned kept = 0xffffffffu;   // bit g: group g takes part
     if (p.topk_group < p.n_group) {
         // 2^x lanes per group find its two largest keys; then the groups are chosen like experts
-        const int gs = p.E / p.n_group;
-        int per = 1;
-        while (per * 2 * p.n_group <= 32) per *= 2;
-        const int g = lane / per, r = lane % per;
+        const int sh = 31 - __clz(32 / p.n_group), per = 1 << sh;
+        const int g = lane >> sh, r = lane & (per - 1);
         unsigned long long a = 0, b = 0;   // largest, second largest
-        if (g < p.n_group) {
+        if (g < p.n_group)
             for (int e = g * gs + r; e < (g + 1) * gs; e += per) {
                 const unsigned long long v = s.key[e];
                 if (v > a) { b = a; a = v; } else if (v > b) b = v;
             }
-        }
         for (int off = per / 2; off >= 1; off >>= 1) {
             const unsigned long long oa = __shfl_xor_sync(0xffffffffu, a, off);
             const unsigned long long ob = __shfl_xor_sync(0xffffffffu, b, off);
@@ -283,10 +348,8 @@ __device__ __forceinline__ bool route_attempt(const RouteScratch& s, const Route
         const bool leader = g < p.n_group && r == 0;
         const bool two = p.group_top == 2 && b > kMaskedKey;
         const double G = two ? key_value(a) + key_value(b) : key_value(a);
-        const unsigned long long gq = leader ? order_key(G) : 0;
-        unsigned long long left = gq;
-        unsigned kept = 0;   // bit g: group g takes part
-        unsigned long long lowest = 0;
+        unsigned long long left = leader ? order_key(G) : 0, lowest = 0;
+        kept = 0;
         for (int j = 0; j < p.topk_group; j++) {
             lowest = warp_max_key(left);
             const int win = (int)__reduce_min_sync(0xffffffffu, left == lowest && left != 0 ? unsigned(g) : 0xffffffffu);
@@ -309,39 +372,38 @@ __device__ __forceinline__ bool route_attempt(const RouteScratch& s, const Route
             const bool sel = open && ((in && G - eg <= high) || (out && G + eg >= low));
             const unsigned lanes = __ballot_sync(0xffffffffu, sel);
             if (lanes) {
-#pragma unroll
-                for (int i = 0; i < VPL; i++) {
-                    const int e = lane + 32 * i, src = e < p.E ? (e / gs) * per : 0;
+                for (int i = 0; 32 * i < p.E; i++) {
+                    const int e = lane + 32 * i, src = e < p.E ? (e / gs) << sh : 0;
                     const double mg = __shfl_sync(0xffffffffu, m, src);
-                    if (e < p.E && ((lanes >> src) & 1u) && !s.exact[e] && key_value(q[i]) >= mg) mark |= 1u << i;
+                    if (e < p.E && ((lanes >> src) & 1u) && !s.exact[e] && key_value(s.key[e]) >= mg) mark |= 1u << i;
                 }
                 return false;
             }
         }
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const int e = lane + 32 * i;
-            if (e < p.E && !((kept >> (e / gs)) & 1u)) q[i] = 0;
-        }
     }
 
+    unsigned taken = 0;                  // of this lane's experts, bit i: lane + 32 i
+    auto left = [&](int i) {             // key of the i-th if it still takes part, else 0
+        const int e = lane + 32 * i;
+        return e < p.E && !((taken >> i) & 1u) && ((kept >> (e / gs)) & 1u) ? s.key[e] : 0ull;
+    };
+    if (p.topk_group == p.n_group) kept = 0xffffffffu;
     unsigned long long my_q = 0;
     my_e = 0;
     for (int j = 0; j < p.k; j++) {
         unsigned long long best = 0;
         int bi = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; i++)
-            if (q[i] > best) { best = q[i]; bi = i; }   // ascending e within the lane: ties keep the lower
+        for (int i = 0; 32 * i < p.E; i++) {
+            const unsigned long long v = left(i);
+            if (v > best) { best = v; bi = i; }   // ascending e within the lane: ties keep the lower
+        }
         const unsigned long long top = warp_max_key(best);
         const int win = (int)__reduce_min_sync(0xffffffffu, best == top ? unsigned(lane + 32 * bi) : 0xffffffffu);
         if (lane == j) {
             my_e = win;
             my_q = top;
         }
-        const int wi = (win & 31) == lane ? win >> 5 : -1;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) q[i] = i == wi ? 0 : q[i];
+        if ((win & 31) == lane) taken |= 1u << (win >> 5);
     }
 
     // Are the ranks safe?  First by plain distances, then by what is known exactly
@@ -350,8 +412,10 @@ __device__ __forceinline__ bool route_attempt(const RouteScratch& s, const Route
     const double last = __shfl_sync(0xffffffffu, c, p.k - 1);
     const unsigned long long near = order_key(last - 2 * eta);
     bool close = lane + 1 < p.k && c - below <= 2 * eta;
-#pragma unroll
-    for (int i = 0; i < VPL; i++) close |= q[i] != 0 && q[i] >= near;
+    for (int i = 0; 32 * i < p.E; i++) {
+        const unsigned long long v = left(i);
+        close |= v != 0 && v >= near;
+    }
     if (!__any_sync(0xffffffffu, close)) return true;
     const double my_eta = s.exact[my_e] ? 0.0 : eta;
     unsigned amb = 0;   // ranks to settle
@@ -362,15 +426,15 @@ __device__ __forceinline__ bool route_attempt(const RouteScratch& s, const Route
     }
     const double last_eta = __shfl_sync(0xffffffffu, my_eta, p.k - 1);
     bool any = false;
-#pragma unroll
-    for (int i = 0; i < VPL; i++)
-        if (q[i] != 0) {
-            const double ei = s.exact[lane + 32 * i] ? 0.0 : eta, m = ei + last_eta;
-            if (m > 0.0 && last - key_value(q[i]) <= m) {
-                any = true;
-                if (ei > 0.0) mark |= 1u << i;
-            }
+    for (int i = 0; 32 * i < p.E; i++) {
+        const unsigned long long v = left(i);
+        if (v == 0) continue;
+        const double ei = s.exact[lane + 32 * i] ? 0.0 : eta, m = ei + last_eta;
+        if (m > 0.0 && last - key_value(v) <= m) {
+            any = true;
+            if (ei > 0.0) mark |= 1u << i;
         }
+    }
     if (__any_sync(0xffffffffu, any)) amb |= 1u << (p.k - 1);
     for (unsigned r = amb; r; r &= r - 1) {
         const int e = __shfl_sync(0xffffffffu, my_e, __ffs(r) - 1);
@@ -381,9 +445,8 @@ __device__ __forceinline__ bool route_attempt(const RouteScratch& s, const Route
 
 // First selection values, in fp32, from s.l; returns eta.  delta: bound on the error of the
 // logits (0: exact).
-template <int VPL>
-__device__ __forceinline__ double route_first_values(const RouteScratch& s, const RouteChoice& p, double delta, int lane,
-                                                     RouteSoftmax& sm) {
+__device__ __noinline__ double route_first_values(const RouteScratch s, const RouteChoice& p, double delta, int lane,
+                                                  RouteSoftmax& sm) {
     double eta;
     float inv = 1.0f;
     if (p.sigmoid) {
@@ -413,10 +476,7 @@ __device__ __forceinline__ double route_first_values(const RouteScratch& s, cons
             eta = (2.3 * delta + 0x1p-17) * (double)inv;
         }
     }
-#pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane + 32 * i;
-        if (e >= p.E) continue;
+    for (int e = lane; e < p.E; e += 32) {
         const double l = s.l[e];
         const float b = p.bias ? __ldg(p.bias + e) : 0.0f;
         unsigned long long q = kMaskedKey;
@@ -433,6 +493,31 @@ __device__ __forceinline__ double route_first_values(const RouteScratch& s, cons
     return eta;
 }
 
+// The true ranks of a close call, whose wanted logits in s.l are exact: the others are far enough
+// from any.  Returns the expert of rank `lane`.  inv: 1 / sum of exp(l - mx) with a bias, else 1.
+__device__ __noinline__ int route_settle(const RouteScratch s, const RouteChoice& p, const RouteClose& close, double mx,
+                                         double inv, int lane) {
+    double v = close.c;
+    if (close.want) {
+        const double l = s.l[close.e];
+        v = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv + (p.bias ? (double)__ldg(p.bias + close.e) : 0.0);
+    }
+    const unsigned long long key = lane < close.n ? order_key(v) : 0;
+    int rank = 0;
+    for (int j = 0; j < close.n; j++) {
+        const unsigned long long kj = __shfl_sync(0xffffffffu, key, j);
+        const int ej = __shfl_sync(0xffffffffu, close.e, j);
+        rank += kj > key || (kj == key && ej < close.e);
+    }
+    __syncwarp();
+    unsigned* order = s.key32;           // (done with by now)
+    if (lane < close.n && rank < p.k) order[rank] = close.e;
+    __syncwarp();
+    const int e = lane < p.k ? (int)order[lane] : 0;
+    __syncwarp();
+    return e;
+}
+
 // The fp64 selection value of expert e from s.l[e].
 __device__ __forceinline__ void route_make_exact(const RouteScratch& s, const RouteChoice& p, const RouteSoftmax& sm, int e) {
     double v = route_score64(s.l[e], p.sigmoid, sm.mx);
@@ -441,21 +526,15 @@ __device__ __forceinline__ void route_make_exact(const RouteScratch& s, const Ro
     s.exact[e] = 1;
 }
 
-// Weights of the chosen experts (my_e: rank `lane`'s, my_l: its logit); inv(): 1 / sum of
-// exp(l - mx) over all experts, asked for by the whole warp where the weights need it.
-template <class Inv>
-__device__ __forceinline__ void route_weights(const RouteChoice& p, double mx, int lane, int my_e, double my_l, Inv inv,
-                                              int32_t* idx_out, float* w_out) {
-    double v = 0.0;
-    if (lane < p.k) {
-        const float b = p.bias ? __ldg(p.bias + my_e) : 0.0f;
-        v = b == -INFINITY ? 0.0 : route_score64(my_l, p.sigmoid, mx);
-    }
+// Weights of the chosen experts (my_e: rank `lane`'s).
+__device__ __noinline__ void route_weights(const RouteScratch s, const RouteChoice& p, double mx, int lane, int my_e, bool masked,
+                                           int32_t* idx_out, float* w_out) {
+    double v = lane < p.k && !masked ? route_score64(s.l[my_e], p.sigmoid, mx) : 0.0;
     if (p.renorm) {
         const double den = warp_sum(v);
         v = den == 0.0 ? 0.0 : v / den;
     } else if (!p.sigmoid) {
-        const double f = inv();
+        const double f = route_softmax_inv(s.l, p.E, mx, lane);
         v = v == 0.0 ? 0.0 : v * f;
     }
     if (lane < p.k) {
@@ -464,15 +543,18 @@ __device__ __forceinline__ void route_weights(const RouteChoice& p, double mx, i
     }
 }
 
-// The whole choice for logits that are exact (s.l complete, __syncwarp done).
-template <int VPL>
+__device__ __forceinline__ bool route_bias_masks(const RouteChoice& p, int e) {
+    return p.bias && __ldg(p.bias + e) == -INFINITY;
+}
+
+// The whole choice in fp64 for logits that are exact (s.l complete, __syncwarp done).
 __device__ __noinline__ void route_choose_exact(const RouteScratch s, const RouteChoice& p, int lane, int32_t* idx_out,
                                                 float* w_out) {
     RouteSoftmax sm;
-    const double eta = route_first_values<VPL>(s, p, 0.0, lane, sm);
+    const double eta = route_first_values(s, p, 0.0, lane, sm);
     unsigned mark;
     int my_e;
-    while (!route_attempt<VPL>(s, p, eta, lane, mark, my_e)) {
+    while (!route_attempt(s, p, eta, lane, mark, my_e)) {
         if (!p.sigmoid && p.bias && !sm.have_inv) {
             sm.inv = route_softmax_inv(s.l, p.E, sm.mx, lane);
             sm.have_inv = true;
@@ -480,22 +562,7 @@ __device__ __noinline__ void route_choose_exact(const RouteScratch s, const Rout
         for (; mark; mark &= mark - 1) route_make_exact(s, p, sm, lane + 32 * (__ffs(mark) - 1));
         __syncwarp();
     }
-    route_weights(p, sm.mx, lane, my_e, s.l[my_e],
-                  [&]() { return sm.have_inv ? sm.inv : route_softmax_inv(s.l, p.E, sm.mx, lane); }, idx_out, w_out);
-    __syncwarp();
-}
-
-// Weights after a certain route_fast, whose logits are lf (given as fp64 by l64 where that is more).
-template <int VPL, class L64>
-__device__ __forceinline__ void route_fast_weights(const float (&lf)[VPL], const RouteChoice& p, float mx, int lane, int my_e,
-                                                   L64 l64, int32_t* idx_out, float* w_out) {
-    const double m = mx;
-    route_weights(p, m, lane, my_e, l64(my_e), [&]() {
-        double sum = 0.0;
-#pragma unroll 1
-        for (int e = lane; e < p.E; e += 32) sum += exp(l64(e) - m);
-        return 1.0 / warp_sum(sum);
-    }, idx_out, w_out);
+    route_weights(s, p, sm.mx, lane, my_e, route_bias_masks(p, my_e), idx_out, w_out);
 }
 
 }  // namespace moe
