@@ -18,7 +18,8 @@ namespace moe {
 int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
                  uint32_t box_bytes, uint32_t box_rows, bool swizzle128);
 
-constexpr int kChooseWarps = 8;          // tokens per CTA of the choosing kernels
+constexpr int kChooseWarps = 8;          // warps per CTA of the kernels for few tokens and given logits
+constexpr int kGemmTokens = 4;           // tokens, a warp each, per CTA of the choice after the GEMM
 constexpr int kSmallTile = 8;            // largest token tile of the fp64 kernel
 constexpr int kSmallT = 16;              // most tokens it takes
 constexpr size_t kCounterBytes = 256;    // its tickets, at the start of the workspace
@@ -45,7 +46,7 @@ __device__ __forceinline__ void choose_row(L64 l64, bool rounded, uint8_t* scrat
 #pragma unroll 4
     for (int e = lane; e < p.E; e += 32) {
         const double l = l64(e);
-        s.fill(e, l, (float)l, p.bias);
+        s.fill(e, l, (float)l, p.bias ? __ldg(p.bias + e) : 0.0f);
         big = max(big, __float_as_uint((float)l) & 0x7FFFFFFFu);
     }
     __syncwarp();
@@ -213,6 +214,17 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void add_f32x2(float& a0, float& a1, float b0, float b1) {
+    asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
+}
+
+// `bytes` (a multiple of 16) of this CTA's shared memory to global memory, asynchronously.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+
 // One CTA: 128 tokens x N experts over Kc of H.  Warp 0 loads (TMA, 128-byte swizzle), warp 1
 // issues the MMAs into two accumulators in turn, a chunk of K each; warps 4-11 add the chunks up
 // in registers (a row and 128 experts a thread), after the sums of squares of a share of W_r;
@@ -323,10 +335,17 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
                     const uint4* row = reinterpret_cast<const uint4*>(sm + s * stage + (r + 64 * h) * 128);
 #pragma unroll
                     for (int c = 0; c < 8; c++) {
-                        float v[8];
-                        unpack8(row[(c + r) & 7], v);   // a quarter warp's rows in different banks
+                        // a quarter warp's rows in different banks; eight squares in bf16, their
+                        // sum in fp32: 2^-6 off at most, which the bound allows for
+                        const uint4 q = row[(c + r) & 7];
+                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                        __nv_bfloat162 p = __float2bfloat162_rn(0.0f);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) sq[h] = fmaf(v[i], v[i], sq[h]);
+                        for (int i = 0; i < 4; i++) {
+                            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&u[i]);
+                            p = __hfma2(v, v, p);
+                        }
+                        sq[h] += __low2float(p) + __high2float(p);
                     }
                 }
             }
@@ -359,9 +378,9 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
                 uint32_t v[16];
                 tmem_ld_32x16(acc + 16 * b, v);
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    sum[b][i] += __uint_as_float(v[i]);
-                    top = fmaxf(top, fabsf(sum[b][i]));
+                for (int i = 0; i < 16; i += 2) {
+                    add_f32x2(sum[b][i], sum[b][i + 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                    top = fmaxf(fmaxf(top, fabsf(sum[b][i])), fabsf(sum[b][i + 1]));
                 }
             }
             tc_fence_before();
@@ -376,17 +395,20 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             if (nt == 0) g.xn[(size_t)rank * g.T + t] = s_sq[r];
             g.xm[((size_t)rank * g.n_tiles + nt) * g.T + t] = s_bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(s_max[r]);
         }
-        if (t < g.T) {
-            float* dst = g.part + ((size_t)rank * g.T + t) * g.Ep + nt * kRgMaxN + half * 128;
+        // the stages are free now: a thread's half row goes through shared memory, so that it
+        // leaves in one piece (its rows 528 bytes apart: different banks)
+        if (width > 0 && t < g.T) {
+            float* row = reinterpret_cast<float*>(sm) + (half * 128 + r) * 132;
 #pragma unroll
-            for (int b = 0; b < 8; b++) {
-                if (16 * b >= width) break;
+            for (int b = 0; b < 8; b++)
 #pragma unroll
-                for (int i = 0; i < 16; i += 8)   // whole 32-byte sectors
-                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * b + i),
-                                 "f"(sum[b][i]), "f"(sum[b][i + 1]), "f"(sum[b][i + 2]), "f"(sum[b][i + 3]),
-                                 "f"(sum[b][i + 4]), "f"(sum[b][i + 5]), "f"(sum[b][i + 6]), "f"(sum[b][i + 7]) : "memory");
-            }
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(row + 16 * b + i) =
+                        make_float4(sum[b][i], sum[b][i + 1], sum[b][i + 2], sum[b][i + 3]);
+            fence_proxy_async_smem();
+            bulk_s2g(g.part + ((size_t)rank * g.T + t) * g.Ep + nt * kRgMaxN + half * 128, row, 4 * min(width, 128));
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
     }
     __syncthreads();
@@ -407,18 +429,19 @@ enum ChooseMode {
 };
 
 struct ChooseShared {
-    int n[kChooseWarps];                      // wanted logits per token
-    int want[kChooseWarps][32];               // their experts (n > 32: all)
-    double got[kChooseWarps][32];             // their values
-    double part[2][kChooseWarps][4];          // the warps' parts of four dot products
+    int n[kGemmTokens];                      // wanted logits per token
+    int want[kGemmTokens][32];               // their experts (n > 32: all)
+    double got[kGemmTokens][32];             // their values
+    double part[2][kGemmTokens][4];          // the warps' parts of four dot products
+    float w2[kGemmTokens];                   // largest |W_e|^2 each warp saw
 };
 
 // The wanted logits of the CTA's tokens in fp64, by all warps: each takes an eighth of H,
 // four dot products at a time.  Values go to got, or to the token's scratch where all are wanted.
-__device__ __forceinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, const uint16_t* x, const uint16_t* wr, int H, int E,
+__device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, const uint16_t* x, const uint16_t* wr, int H, int E,
                                              int t0, int warp, int lane) {
     int total = 0;
-    for (int h = 0; h < kChooseWarps; h++) total += sh.n[h];
+    for (int h = 0; h < kGemmTokens; h++) total += sh.n[h];
     for (int j0 = 0, buf = 0; j0 < total; j0 += 4, buf ^= 1) {
         const uint4 *xr[4], *wrow[4];
 #pragma unroll
@@ -431,7 +454,7 @@ __device__ __forceinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch,
         }
         double acc[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 1
-        for (int c = warp * 32 + lane; c < H / 8; c += 32 * kChooseWarps) {
+        for (int c = warp * 32 + lane; c < H / 8; c += 32 * kGemmTokens) {
             uint4 xq[4], wq[4];
 #pragma unroll
             for (int a = 0; a < 4; a++) {
@@ -452,7 +475,7 @@ __device__ __forceinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch,
         __syncthreads();
         if (threadIdx.x < 4 && j0 + (int)threadIdx.x < total) {
             double sum = 0.0;
-            for (int w = 0; w < kChooseWarps; w++) sum += sh.part[buf][w][threadIdx.x];
+            for (int w = 0; w < kGemmTokens; w++) sum += sh.part[buf][w][threadIdx.x];
             int h = 0, j = j0 + threadIdx.x;
             while (j >= sh.n[h]) j -= sh.n[h++];
             if (sh.n[h] > 32) RouteScratch(scratch + h * RouteScratch::bytes(E), E).l[j] = sum;
@@ -463,13 +486,13 @@ __device__ __forceinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch,
 }
 
 // One warp per token.
-__global__ void __launch_bounds__(kChooseWarps * 32)
+__global__ void __launch_bounds__(kGemmTokens * 32, 4)
 route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, RouteGemmArgs g, RouteChoice p,
                          int32_t* __restrict__ idx, float* __restrict__ wout) {
     extern __shared__ __align__(16) uint8_t sm_raw[];
     __shared__ ChooseShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t0 = blockIdx.x * kChooseWarps, t = t0 + warp;
+    const int t0 = blockIdx.x * kGemmTokens, t = t0 + warp;
     const RouteScratch s(sm_raw + warp * RouteScratch::bytes(p.E), p.E);
     int32_t* idx_t = idx + size_t(t) * p.k;
     float* w_t = wout + size_t(t) * p.k;
@@ -489,39 +512,59 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
         route_weights(s, p, sm.mx, lane, my_e, route_bias_masks(p, my_e), idx_t, w_t);
         mode = kDone;
     };
+    // the norms and largest sums, on their way while the logits are read
+    float w2 = 0.0f, xn = 0.0f, xm = 0.0f;
+    for (int e = threadIdx.x; e < p.E; e += kGemmTokens * 32) {
+        const float v = __ldg(g.wn + e);
+        w2 = !(v <= w2) ? v : w2;               // a NaN stays
+    }
     if (t < g.T) {
-        float wmax = 0.0f, xn = 0.0f, xm = 0.0f;
+        if (lane < g.split) xn = __ldg(g.xn + (size_t)lane * g.T + t);
+        // (the sum over the tiles of experts is more than their largest)
+        for (int c = lane; c < g.split * g.n_tiles; c += 32) xm += __ldg(g.xm + (size_t)c * g.T + t);
+#pragma unroll 1
         for (int e = 4 * lane; e < p.E; e += 128) {
             const float* col = g.part + (size_t)t * g.Ep + e;      // (rows are padded to 32)
-            float4 l = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int c = 0; c < g.split; c++) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(col + (size_t)c * g.T * g.Ep));
-                l.x += v.x; l.y += v.y; l.z += v.z; l.w += v.w;
+            float bias[4], l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; i++) bias[i] = p.bias && e + i < p.E ? __ldg(p.bias + e + i) : 0.0f;
+            for (int c0 = 0; c0 < g.split; c0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int c = 0; c < 8; c++)
+                    v[c] = c0 + c < g.split ? __ldg(reinterpret_cast<const float4*>(col + (size_t)(c0 + c) * g.T * g.Ep))
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    l[0] += v[c].x; l[1] += v[c].y; l[2] += v[c].z; l[3] += v[c].w;
+                }
             }
-            const float v[4] = {l.x, l.y, l.z, l.w};
+            if (p.E % 4 == 0) {     // four at once: a quarter of the shared-memory conflicts
+                *reinterpret_cast<double2*>(s.l + e) = make_double2(l[0], l[1]);
+                *reinterpret_cast<double2*>(s.l + e + 2) = make_double2(l[2], l[3]);
+                *reinterpret_cast<float4*>(s.l32 + e) = make_float4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<float4*>(s.bias + e) = make_float4(bias[0], bias[1], bias[2], bias[3]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                if (e + i < p.E) s.fill(e + i, v[i], v[i], p.bias);
+                for (int i = 0; i < 4; i++)
+                    if (e + i < p.E) s.fill(e + i, l[i], l[i], bias[i]);
+            }
         }
-        for (int c = lane; c < g.split; c += 32) xn += __ldg(g.xn + (size_t)c * g.T + t);
-        // (the sum over the tiles of experts is more than their largest: a NaN stays)
-        for (int c = lane; c < g.split * g.n_tiles; c += 32) xm += __ldg(g.xm + (size_t)c * g.T + t);
+    }
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            xn += __shfl_xor_sync(0xffffffffu, xn, off);
-            xm += __shfl_xor_sync(0xffffffffu, xm, off);
-        }
-        for (int e = lane; e < p.E; e += 32) {
-            const float w2 = __ldg(g.wn + e);
-            wmax = !(w2 <= wmax) ? w2 : wmax;
-        }
+    for (int off = 16; off >= 1; off >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, w2, off);
+        w2 = !(o <= w2) ? o : w2;
+        xn += __shfl_xor_sync(0xffffffffu, xn, off);
+        xm += __shfl_xor_sync(0xffffffffu, xm, off);
+    }
+    if (lane == 0) sh.w2[warp] = w2;
+    __syncthreads();
+    if (t < g.T) {
+        float wmax = 0.0f;
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            const float o = __shfl_xor_sync(0xffffffffu, wmax, off);
-            wmax = !(o <= wmax) ? o : wmax;
-        }
-        delta = (float)(1.001 * (kGemmError * sqrt((double)xn * (double)wmax) +
+        for (int i = 0; i < kGemmTokens; i++) wmax = !(sh.w2[i] <= wmax) ? sh.w2[i] : wmax;
+        delta = (float)(1.02 * (kGemmError * sqrt((double)xn * (double)wmax) +
                                  0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
         if (!(delta <= 0.05f)) {
             mode = kAll;
@@ -695,14 +738,15 @@ static int launch_large(const RouteCall& r) {
     if ((rc = make_tmap_2d(&mx, r.x, size_t(r.H) * 2, r.T, size_t(r.H) * 2, 128, 128, true))) return rc;
     if ((rc = make_tmap_2d(&mw, r.wr, size_t(r.H) * 2, E, size_t(r.H) * 2, 128, g.N, true))) return rc;
     static bool gdone[64] = {}, cdone[64] = {};
-    const int smem = kRgStages * (16384 + g.N * 128) + 1024;
+    // (the sums leave through 2 x 128 half rows of 528 bytes)
+    const int smem = std::max(kRgStages * (16384 + g.N * 128), 256 * 528) + 1024;
     MOE_CUDA_TRY(raise_smem(route_gemm_kernel, kRgStages * (16384 + kRgMaxN * 128) + 1024, gdone));
     const dim3 grid(((r.T + 127) / 128) * g.n_tiles * g.split);
     MOE_CUDA_TRY(launch_pdl(route_gemm_kernel, grid, dim3(kRgThreads), smem, r.s, mx, mw, g));
     auto kern = route_gemm_choose_kernel;
-    MOE_CUDA_TRY(raise_smem(kern, (int)(kChooseWarps * RouteScratch::bytes(kMaxE)), cdone));
-    MOE_CUDA_TRY(launch_pdl(kern, dim3((r.T + kChooseWarps - 1) / kChooseWarps), dim3(kChooseWarps * 32),
-                            kChooseWarps * RouteScratch::bytes(E), r.s, r.x, r.wr, g, r.p, r.idx, r.w));
+    MOE_CUDA_TRY(raise_smem(kern, (int)(kGemmTokens * RouteScratch::bytes(kMaxE)), cdone));
+    MOE_CUDA_TRY(launch_pdl(kern, dim3((r.T + kGemmTokens - 1) / kGemmTokens), dim3(kGemmTokens * 32),
+                            kGemmTokens * RouteScratch::bytes(E), r.s, r.x, r.wr, g, r.p, r.idx, r.w));
     return MOE_OK;
 }
 

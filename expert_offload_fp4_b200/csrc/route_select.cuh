@@ -71,10 +71,10 @@ struct RouteScratch {
         : l(static_cast<double*>(p)), l32(reinterpret_cast<float*>(l + E)), bias(l32 + 2 * E),
           key32(reinterpret_cast<unsigned*>(l32 + E)), key(reinterpret_cast<unsigned long long*>(l32)),
           exact(reinterpret_cast<unsigned char*>(bias)) {}
-    __device__ __forceinline__ void fill(int e, double v, float v32, const float* b) const {
+    __device__ __forceinline__ void fill(int e, double v, float v32, float b) const {
         l[e] = v;
         l32[e] = v32;
-        bias[e] = b ? __ldg(b + e) : 0.0f;
+        bias[e] = b;
     }
 };
 
@@ -382,12 +382,9 @@ __device__ __noinline__ bool route_attempt(const RouteScratch s, const RouteChoi
         }
     }
 
-    unsigned taken = 0;                  // of this lane's experts, bit i: lane + 32 i
-    auto left = [&](int i) {             // key of the i-th if it still takes part, else 0
-        const int e = lane + 32 * i;
-        return e < p.E && !((taken >> i) & 1u) && ((kept >> (e / gs)) & 1u) ? s.key[e] : 0ull;
-    };
-    if (p.topk_group == p.n_group) kept = 0xffffffffu;
+    unsigned part = 0;                   // which of this lane's experts take part, bit i: lane + 32 i
+    for (int i = 0; lane + 32 * i < p.E; i++) part |= ((kept >> ((lane + 32 * i) / gs)) & 1u) << i;
+    auto left = [&](int i) { return (part >> i) & 1u ? s.key[lane + 32 * i] : 0ull; };
     unsigned long long my_q = 0;
     my_e = 0;
     for (int j = 0; j < p.k; j++) {
@@ -403,7 +400,7 @@ __device__ __noinline__ bool route_attempt(const RouteScratch s, const RouteChoi
             my_e = win;
             my_q = top;
         }
-        if ((win & 31) == lane) taken |= 1u << (win >> 5);
+        if ((win & 31) == lane) part &= ~(1u << (win >> 5));
     }
 
     // Are the ranks safe?  First by plain distances, then by what is known exactly
