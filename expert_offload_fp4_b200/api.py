@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+from dataclasses import dataclass
 
 import numpy as np
 import torch
@@ -169,6 +170,17 @@ def _call(name, tensors, stream, *args):
         L.check(name, rc)
 
 
+@dataclass(frozen=True)
+class GroupedRouting:
+    """How a layer chooses its experts (the options of route_grouped)."""
+    score: str = "sigmoid"
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+
 _SCORE = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 _TYPE = {torch.bfloat16: L.MOE_BF16, torch.float32: L.MOE_F32}
 
@@ -276,6 +288,22 @@ def fp4_swiglu(x, gate, up, h, status, stream=None):
           _TYPE[x.dtype], ldx, T, h.data_ptr(), ldh, _status(status))
 
 
+class SharedExpert:
+    """The always-active SwiGLU expert beside a layer's routed ones: gate and up [I, H],
+    down [H, I] as FP4Weight."""
+
+    def __init__(self, gate, up, down):
+        _need((gate.N, gate.K, gate.fmt) == (up.N, up.K, up.fmt), "gate and up must have one shape and format")
+        _need((down.N, down.K) == (gate.K, gate.N), "down must be [H, I] for gate and up [I, H]")
+        self.gate, self.up, self.down = gate, up, down
+        self.I, self.H = gate.N, gate.K
+
+    def add_to(self, x, h, y, status, stream=None):
+        """y [T, H] bf16 += the expert's output for x [T, H] bf16; h [T, I] fp32 scratch."""
+        fp4_swiglu(x, self.gate, self.up, h, status, stream=stream)
+        fp4_linear(h, self.down, y, status, add=y, stream=stream)
+
+
 class Lookup:
     """Host-side result of one slot lookup (arrays sized for the call)."""
 
@@ -353,6 +381,20 @@ def decode_layer(pool, layer, x, wr, bias, renormalize, idx, w, slot_of, y_part,
         _p(slot_of), _p(y_part), _p(y), _p(status), _p(ws), ws.numel(),
         C.byref(lookup.res) if lookup is not None else None, ev0, ev1, 1 if overlap else 0,
         _s(stream), _s(cs)))
+
+
+def decode_layer_routed(pool, layer, x, idx, w, slot_of, y_part, y, status, lookup=None, copy_events=None,
+                        overlap=True, stream=None, copy_stream=None):
+    """moe_decode_layer_routed: lookup, FFN, miss copies and combine of one layer for
+    idx and w that another router wrote on the same stream."""
+    if copy_stream is None:
+        raise ValueError("decode_layer_routed needs a copy_stream of its own (torch.cuda.Stream())")
+    ev0, ev1 = (None, None) if copy_events is None else (C.c_void_p(copy_events[0].cuda_event),
+                                                        C.c_void_p(copy_events[1].cuda_event))
+    L.check("moe_decode_layer_routed", pool.lib.moe_decode_layer_routed(
+        pool.handle, int(layer), _p(x), x.shape[0], _p(idx), _p(w), _p(slot_of), _p(y_part), _p(y), _p(status),
+        C.byref(lookup.res) if lookup is not None else None, ev0, ev1, 1 if overlap else 0, _s(stream),
+        _s(copy_stream)))
 
 
 def decode_resident(pool, layer0, x, wr, bias, renormalize, idx, w, slot_of, y_part, y, status, stream=None):

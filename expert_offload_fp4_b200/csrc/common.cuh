@@ -64,6 +64,8 @@ int preload_ffn_kernels();
 int preload_gemm_kernels();
 int preload_prefill_kernels();
 int preload_pull_kernels();
+int preload_route_grouped_kernels();
+int preload_fp4_linear_kernels();
 cudaError_t launch_pull(const uint8_t* src_d, uint8_t* dst, size_t bytes, int num_sms, cudaStream_t s);
 // The router fused into a resident decode FFN: router weights [E, H] bf16, bias
 // [E] or null, and the caller's idx / w, which the FFN writes.

@@ -697,7 +697,18 @@ static int check_weight(const moe_fp4_weight* w) {
     if (!w || !w->codes || !w->scales) return fail(MOE_EINVAL, "fp4 weight: null pointer");
     if (w->fmt != MOE_MXFP4 && w->fmt != MOE_NVFP4) return fail(MOE_EINVAL, "fp4 weight: unknown format");
     if (w->N <= 0 || w->K <= 0 || w->K % 32) return fail(MOE_EINVAL, "fp4 weight: need N > 0 and K a positive multiple of 32");
+    if (w->N > (1 << 30)) return fail(MOE_EINVAL, "fp4 weight: N too large");
     if (reinterpret_cast<uintptr_t>(w->codes) & 15) return fail(MOE_EINVAL, "fp4 weight: codes must be 16-byte aligned");
+    return MOE_OK;
+}
+
+// The digits of x, 4 bytes an element of a token pair's columns, fill at most 128 KiB of each of a
+// cluster's 8 CTAs.
+static int check_tokens(int T, int K) {
+    if (T <= 0 || T > kMaxDecodeT) return fail(MOE_EINVAL, "fp4: T must be in [1, 16]");
+    const long long Tp = (T + 1) & ~1;
+    if (Tp * ((K + kLinKT - 1) / kLinKT * kLinKT) > 262144)
+        return fail(MOE_EINVAL, "fp4: K too large for this many tokens (K * T, T rounded up to even, at most 262144)");
     return MOE_OK;
 }
 
@@ -754,7 +765,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
         const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 10 * rounds;
         if (!bestC || cost < best) { best = cost; bestC = C; }
     }
-    if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens (K * T, T rounded up to even, at most 262144)");
+    if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
     a.C = bestC;
     const int kt = (KTall + a.C - 1) / a.C;
     a.Kc = kt * kLinKT;
@@ -841,6 +852,20 @@ static int launch_linear(LinArgs& a, const moe_fp4_weight* w0, const moe_fp4_wei
     }
 }
 
+// Load the kernels now (module loading may wait for the device).
+int preload_fp4_linear_kernels() {
+    cudaFuncAttributes fa;
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_MXFP4, 0, 0>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_MXFP4, 0, 1>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_MXFP4, 1, 0>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_MXFP4, 1, 1>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_NVFP4, 0, 0>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_NVFP4, 0, 1>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_NVFP4, 1, 0>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, fp4_linear_kernel<MOE_NVFP4, 1, 1>));
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -849,7 +874,7 @@ extern "C" int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type
                               long long ld_add, void* y, int y_type, long long ldy, int* status, void* stream) {
     int rc = check_weight(w);
     if (rc) return rc;
-    if (T <= 0 || T > kMaxDecodeT) return fail(MOE_EINVAL, "fp4 linear: T must be in [1, 16]");
+    if ((rc = check_tokens(T, w->K))) return rc;
     if (!status) return fail(MOE_EINVAL, "fp4 linear: null status");
     if ((rc = check_rows(x, x_type, ldx, w->K, T, "x"))) return rc;
     if ((rc = check_rows(y, y_type, ldy, w->N, T, "y"))) return rc;
@@ -871,7 +896,7 @@ extern "C" int moe_fp4_swiglu(const moe_fp4_weight* gate, const moe_fp4_weight* 
     if (rc || (rc = check_weight(up))) return rc;
     if (gate->N != up->N || gate->K != up->K || gate->fmt != up->fmt)
         return fail(MOE_EINVAL, "fp4 swiglu: gate and up must have one shape and format");
-    if (T <= 0 || T > kMaxDecodeT) return fail(MOE_EINVAL, "fp4 swiglu: T must be in [1, 16]");
+    if ((rc = check_tokens(T, gate->K))) return rc;
     if (!status) return fail(MOE_EINVAL, "fp4 swiglu: null status");
     if ((rc = check_rows(x, x_type, ldx, gate->K, T, "x"))) return rc;
     if ((rc = check_rows(h, MOE_F32, ldh, gate->N, T, "h"))) return rc;

@@ -11,16 +11,10 @@
 
 using namespace moe;
 
-extern "C" int moe_decode_layer(moe_pool* p, int layer, const void* x_bf16, int T, const void* wr_bf16,
-                                const float* bias, int renormalize, int32_t* idx, float* w,
-                                int32_t* slot_of, float* y_part, void* y_bf16, int* status,
-                                void* route_ws, size_t route_ws_bytes, moe_lookup_result* res,
-                                void* copy_start, void* copy_end, int overlap, void* stream,
-                                void* copy_stream) {
-    if (!p) return fail(MOE_EINVAL, "null pool");
-    // with overlap the FFN waits for copies issued after it: they need their own stream
-    if (overlap && (copy_stream == stream || copy_stream == nullptr))
-        return fail(MOE_EINVAL, "decode layer: copy_stream must be a stream other than the compute stream");
+// The sequence after the router: lookup, FFN with the combine, miss copies.
+static int routed_layer(moe_pool* p, int layer, const void* x_bf16, int T, const int32_t* idx, const float* w,
+                        int32_t* slot_of, float* y_part, void* y_bf16, int* status, moe_lookup_result* res,
+                        void* copy_start, void* copy_end, int overlap, void* stream, void* copy_stream) {
     const moe_config& c = p->cfg;
     // the caller's result arrays, else local ones of the largest size a call needs
     int32_t uniq_l[kMaxE], hit_l[kMaxE];
@@ -36,9 +30,7 @@ extern "C" int moe_decode_layer(moe_pool* p, int layer, const void* x_bf16, int 
         if (copy_end) MOE_CUDA_TRY(cudaEventRecord((cudaEvent_t)copy_end, cs));
         return MOE_OK;
     };
-    int rc = moe_route(x_bf16, wr_bf16, bias, T, c.H, c.E, c.k, renormalize, idx, w, route_ws,
-                       route_ws_bytes, stream);
-    if (rc) return rc;
+    int rc;
     if (!overlap) {
         // misses streamed before the FFN is enqueued (for tools that serialise kernels)
         if ((rc = moe_slot_lookup(p, layer, idx, T, c.k, slot_of, r, stream))) return rc;
@@ -52,6 +44,39 @@ extern "C" int moe_decode_layer(moe_pool* p, int layer, const void* x_bf16, int 
     if (rc) return rc;
     if (rc2) return rc2;
     return copies();
+}
+
+// With overlap the FFN waits for copies issued after it: they need their own stream.
+static int check_layer(const moe_pool* p, int overlap, void* stream, void* copy_stream) {
+    if (!p) return fail(MOE_EINVAL, "null pool");
+    if (overlap && (copy_stream == stream || copy_stream == nullptr))
+        return fail(MOE_EINVAL, "decode layer: copy_stream must be a stream other than the compute stream");
+    return MOE_OK;
+}
+
+extern "C" int moe_decode_layer(moe_pool* p, int layer, const void* x_bf16, int T, const void* wr_bf16,
+                                const float* bias, int renormalize, int32_t* idx, float* w,
+                                int32_t* slot_of, float* y_part, void* y_bf16, int* status,
+                                void* route_ws, size_t route_ws_bytes, moe_lookup_result* res,
+                                void* copy_start, void* copy_end, int overlap, void* stream,
+                                void* copy_stream) {
+    int rc = check_layer(p, overlap, stream, copy_stream);
+    if (rc) return rc;
+    const moe_config& c = p->cfg;
+    if ((rc = moe_route(x_bf16, wr_bf16, bias, T, c.H, c.E, c.k, renormalize, idx, w, route_ws, route_ws_bytes, stream)))
+        return rc;
+    return routed_layer(p, layer, x_bf16, T, idx, w, slot_of, y_part, y_bf16, status, res, copy_start, copy_end, overlap,
+                        stream, copy_stream);
+}
+
+extern "C" int moe_decode_layer_routed(moe_pool* p, int layer, const void* x_bf16, int T, const int32_t* idx,
+                                       const float* w, int32_t* slot_of, float* y_part, void* y_bf16, int* status,
+                                       moe_lookup_result* res, void* copy_start, void* copy_end, int overlap,
+                                       void* stream, void* copy_stream) {
+    const int rc = check_layer(p, overlap, stream, copy_stream);
+    if (rc) return rc;
+    return routed_layer(p, layer, x_bf16, T, idx, w, slot_of, y_part, y_bf16, status, res, copy_start, copy_end, overlap,
+                        stream, copy_stream);
 }
 
 // All-resident decode of consecutive layers (post.smzdm.com/p/aomxznrn,

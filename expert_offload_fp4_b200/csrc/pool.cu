@@ -185,7 +185,8 @@ extern "C" int moe_pool_create(const moe_config* cfg, moe_pool** out) {
         return rc;
     }
     if ((rc = preload_router_kernels()) || (rc = preload_lookup_kernels()) || (rc = preload_ffn_kernels()) ||
-        (rc = preload_gemm_kernels()) || (rc = preload_prefill_kernels()) || (rc = preload_pull_kernels())) {
+        (rc = preload_gemm_kernels()) || (rc = preload_prefill_kernels()) || (rc = preload_pull_kernels()) ||
+        (rc = preload_route_grouped_kernels()) || (rc = preload_fp4_linear_kernels())) {
         moe_pool_destroy(p);
         return rc;
     }

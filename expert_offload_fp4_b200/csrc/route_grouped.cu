@@ -767,6 +767,19 @@ static int launch_select(const void* logits, int bf16, long long ld, int T, cons
     return MOE_OK;
 }
 
+// Load the kernels now (module loading may wait for the device).
+int preload_route_grouped_kernels() {
+    cudaFuncAttributes fa;
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<1>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<2>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<4>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<8>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_kernel));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_choose_kernel));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_select_kernel));
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;

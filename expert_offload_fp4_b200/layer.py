@@ -8,15 +8,24 @@ engine streams the misses, whose CTAs wait for the slot's ready ticket.
 """
 from __future__ import annotations
 
+from dataclasses import asdict
+
 import torch
 
 from . import api
 
 
 class DecodeLayer:
-    def __init__(self, pool: api.Pool, T: int, device="cuda", renormalize=1, overlap=True):
+    """router: None for moe_route's gate (softmax over the chosen or over all experts), or
+    an api.GroupedRouting: sigmoid or softmax scores, the bias steering only the choice,
+    groups of experts."""
+
+    def __init__(self, pool: api.Pool, T: int, device="cuda", renormalize=1, overlap=True, router=None):
         if T > pool.max_tokens:
             raise ValueError("T exceeds the pool's max_tokens")
+        self.router = router
+        self._options = None if router is None else asdict(router)
+        self._h = None       # the shared expert's hidden activations, grown as needed
         # overlap=False issues the miss copies before the FFN launch (the host waits
         # for the lookup first): slower, but safe under tools that serialise kernels
         self.pool, self.T, self.renormalize, self.overlap = pool, T, renormalize, overlap
@@ -27,7 +36,8 @@ class DecodeLayer:
         self.y_part = torch.empty((T, k, H), dtype=torch.float32, device=device)
         self.y = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self.ws = torch.zeros(api.route_workspace_bytes(T, E), dtype=torch.uint8, device=device)
+        ws_bytes = api.route_workspace_bytes if router is None else api.route_grouped_workspace_bytes
+        self.ws = torch.zeros(ws_bytes(T, E), dtype=torch.uint8, device=device)
         self.lookup = api.Lookup(min(T * k, E))
         self.copy_stream = torch.cuda.Stream(device=device)
         # optional timing hooks: lists that receive (start, end) CUDA events recorded
@@ -46,15 +56,35 @@ class DecodeLayer:
                 e.record(self.copy_stream)
             self._spare_events.append(ev)
 
-    def __call__(self, layer, x, wr, bias, stream=None):
+    def __call__(self, layer, x, wr, bias, stream=None, shared=None):
         """x [T, H] bf16, wr [E, H] bf16, bias [E] fp32 (or None), all on the device.
-        Returns y [T, H] bf16 (a buffer reused by the next call).
+        Returns y [T, H] bf16 (a buffer reused by the next call).  shared: an
+        api.SharedExpert whose output is added to the routed experts'.
 
         Order: route, lookup, FFN and combine are enqueued back to back on the
         compute stream; then the host collects the lookup's miss list and drives
         the copy engine.  The FFN's CTAs on resident experts run at once; those on
         missed experts wait (bounded) for the slot's ready ticket that the copy
         stream writes after each expert's block lands."""
+        if shared is None:
+            return self._routed(layer, x, wr, bias, stream)
+        if shared.H != self.pool.H:
+            raise ValueError("the shared expert's H differs from the pool's")
+        # allocated before anything is launched: an FFN may be waiting for copies later
+        if self._h is None or self._h.numel() < self.T * shared.I:
+            self._h = torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device)
+        h = self._h[:self.T * shared.I].view(self.T, shared.I)
+        self._routed(layer, x, wr, bias, stream)
+        shared.add_to(x, h, self.y, self.status, stream)
+        return self.y
+
+    def _route(self, x, wr, bias, stream):
+        if self.router is None:
+            api.route(x, wr, bias, self.pool.k, self.renormalize, self.idx, self.w, self.ws, stream)
+        else:
+            api.route_grouped(x, wr, self.idx, self.w, self.ws, bias=bias, stream=stream, **self._options)
+
+    def _routed(self, layer, x, wr, bias, stream):
         p = self.pool
         if self.ffn_events is None:
             # the whole layer in one native call
@@ -63,15 +93,21 @@ class DecodeLayer:
                 if not self._spare_events:
                     self.reserve_copy_events(1)
                 ev = self._spare_events[-1]
-            api.decode_layer(p, layer, x, wr, bias, self.renormalize, self.idx, self.w, self.slot_of,
-                             self.y_part, self.y, self.status, self.ws, lookup=self.lookup,
-                             copy_events=ev, overlap=self.overlap, stream=stream,
-                             copy_stream=self.copy_stream)
+            if self.router is None:
+                api.decode_layer(p, layer, x, wr, bias, self.renormalize, self.idx, self.w, self.slot_of,
+                                 self.y_part, self.y, self.status, self.ws, lookup=self.lookup,
+                                 copy_events=ev, overlap=self.overlap, stream=stream,
+                                 copy_stream=self.copy_stream)
+            else:
+                self._route(x, wr, bias, stream)
+                api.decode_layer_routed(p, layer, x, self.idx, self.w, self.slot_of, self.y_part, self.y,
+                                        self.status, lookup=self.lookup, copy_events=ev, overlap=self.overlap,
+                                        stream=stream, copy_stream=self.copy_stream)
             if ev is not None and self.lookup.n_miss:
                 self.copy_events.append((self._spare_events.pop(), self.lookup.n_miss))
             return self.y
         # step by step, with events around the FFN launch
-        api.route(x, wr, bias, p.k, self.renormalize, self.idx, self.w, self.ws, stream)
+        self._route(x, wr, bias, stream)
         if not self.overlap:
             api.slot_lookup(p, layer, self.idx, self.slot_of, self.lookup, stream)
             if self.lookup.n_miss:

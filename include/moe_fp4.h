@@ -271,8 +271,11 @@ int moe_route_select(const void* logits, int type, long long ld, const float* bi
  * x [T, K] of x_type (rows 16-byte aligned), y [T, N] of y_type, add NULL or [T, N]
  * of y_type (it may be y itself: y += W x; otherwise no output may overlap an
  * input); row strides ldx, ld_add, ldy in elements.  Sums in fp32, one rounding to
- * y_type at the end.  T from 1 to 16.  Bounded device waits set bit 16 of *status
- * (device int, caller-zeroed) on timeout.  Errors: MOE_EINVAL. */
+ * y_type at the end; x enters to 2^-22 of its largest element in the token (bf16
+ * elements down to 2^-14 of it exactly).  A NaN or infinite element makes all of
+ * its token's outputs NaN.  T from 1 to 16; K * T (K rounded up to 256, T to even) at most 262144.
+ * Bounded device waits set bit 16 of *status (device int, caller-zeroed) on timeout.
+ * Errors: MOE_EINVAL. */
 int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type, long long ldx, int T, const void* add,
                    long long ld_add, void* y, int y_type, long long ldy, int* status, void* stream);
 
@@ -454,6 +457,16 @@ int moe_decode_layer(moe_pool* pool, int layer, const void* x_bf16, int T, const
                      float* y_part, void* y_bf16, int* status, void* route_ws,
                      size_t route_ws_bytes, moe_lookup_result* res, void* copy_start,
                      void* copy_end, int overlap, void* stream, void* copy_stream);
+
+/* moe_decode_layer without its router: idx and w [T, k] (k of the pool) are inputs, written
+ * earlier on `stream` by another router (moe_route_grouped, moe_route_select); every index
+ * within [0, E).  x must be complete before the kernel that
+ * precedes the call on `stream` starts (it is, when the router ran on x).  Otherwise the
+ * arguments, rules and errors of moe_decode_layer. */
+int moe_decode_layer_routed(moe_pool* pool, int layer, const void* x_bf16, int T, const int32_t* idx,
+                            const float* w, int32_t* slot_of, float* y_part, void* y_bf16, int* status,
+                            moe_lookup_result* res, void* copy_start, void* copy_end, int overlap,
+                            void* stream, void* copy_stream);
 
 /* All-resident decode of layers layer0 .. layer0+n_layers-1 (post.smzdm.com/p/
  * aomxznrn, "FreeToken干的事": decode runs on its own bandwidth-bound path): one

@@ -99,6 +99,9 @@ def test_fp4_calls_refuse_bad_arguments(m):
     linear(b"aligned", weight(codes=p + 4))
     linear(b"T must", T=0)
     linear(b"T must", T=17)
+    linear(b"K too large", weight(K=131072 + 32), T=1, ldx=1 << 20)
+    linear(b"K too large", weight(K=16416), T=15, ldx=1 << 20)
+    linear(b"N too large", weight(N=(1 << 30) + 1))
     linear(b"null x", x=None)
     linear(b"null y", y=None)
     linear(b"null status", st=None)
@@ -172,3 +175,22 @@ def test_reference_choice_on_a_hand_worked_token():
     i, w = choose(l, 2, bias=[0, 0, 0, 0, 1.0, 0], renormalize=False)
     assert i.tolist() == [[4, 0]]
     np.testing.assert_allclose(w, [[0.3, 0.6]], rtol=1e-12)
+
+
+def test_shared_expert_and_routed_layer_refusals(m):
+    from types import SimpleNamespace as N
+    g = N(N=64, K=128, fmt="nvfp4")
+    assert m.SharedExpert(g, g, N(N=128, K=64, fmt="mxfp4")).I == 64
+    for bad in (N(N=64, K=96, fmt="nvfp4"), N(N=64, K=128, fmt="mxfp4")):
+        with pytest.raises(ValueError, match="one shape and format"):
+            m.SharedExpert(g, bad, N(N=128, K=64, fmt="nvfp4"))
+    with pytest.raises(ValueError, match="down"):
+        m.SharedExpert(g, g, N(N=64, K=128, fmt="nvfp4"))
+    L, E = m._lib.load(), m._lib
+    buf = (C.c_uint8 * 64)()
+    p, s1 = C.cast(buf, C.c_void_p), C.c_void_p(0x1000)
+    call = lambda pool, stream, cs: L.moe_decode_layer_routed(pool, 0, p, 1, p, p, p, p, p, p, None, None, None, 1,
+                                                              stream, cs)
+    assert call(None, None, s1) == E.MOE_EINVAL and b"null pool" in L.moe_last_error()
+    assert call(p, s1, s1) == E.MOE_EINVAL and b"copy_stream" in L.moe_last_error()
+    assert call(p, s1, None) == E.MOE_EINVAL and b"copy_stream" in L.moe_last_error()
