@@ -147,6 +147,9 @@ def _rows(t, dtypes, rows, cols, what):
     return ld if rows > 1 else cols
 
 
+_functions = {}
+
+
 def _call(name, tensors, stream, *args):
     """Library call on the device that holds all of `tensors`, on `stream` or that
     device's current stream."""
@@ -160,8 +163,10 @@ def _call(name, tensors, stream, *args):
         raise ValueError(f"{name}: the stream belongs to another device than the tensors")
     else:
         handle = stream.cuda_stream
-    fn = getattr(L.load(), name)
-    if torch.cuda.current_device() == dev:
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(L.load(), name)
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

@@ -64,7 +64,8 @@ __device__ __forceinline__ void choose_row(L64 l64, bool rounded, uint8_t* scrat
     }
     if (st == kRouteClose) {
         const double inv = !p.sigmoid && p.bias ? route_softmax_inv(s.l, p.E, mx, lane) : 1.0;
-        my_e = route_settle(s, p, close, mx, inv, lane);
+        bool sure;
+        my_e = route_settle(s, p, close, mx, inv, 0.0, lane, sure);
         masked = route_bias_masks(p, my_e);
     }
     route_weights(s, p, mx, lane, my_e, masked, idx_out, w_out);
@@ -574,10 +575,10 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
             __syncwarp();
             if (st == kRouteCertain) {
                 route_weights(s, p, mx, lane, my_e, masked, idx_t, w_t);
-            } else if (!p.sigmoid && p.bias) {
-                mode = kAll;                 // the denominator hangs on every logit
             } else if (st == kRouteClose) {
                 mode = kRanks;
+            } else if (!p.sigmoid && p.bias) {
+                mode = kAll;                 // the denominator hangs on every logit
             } else {
                 eta = route_first_values(s, p, delta, lane, sm);
                 attempt();
@@ -617,9 +618,13 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
         } else if (mode == kRanks) {
             if (close.want) s.l[close.e] = sh.got[warp][at];
             __syncwarp();
-            my_e = route_settle(s, p, close, mx, 1.0, lane);
-            route_weights(s, p, mx, lane, my_e, route_bias_masks(p, my_e), idx_t, w_t);
-            mode = kDone;
+            // (a softmax's denominator: to the error of its logits)
+            const bool common = !p.sigmoid && p.bias;
+            bool sure;
+            my_e = route_settle(s, p, close, mx, common ? route_softmax_inv(s.l, p.E, mx, lane) : 1.0,
+                                common ? 1.1 * delta : 0.0, lane, sure);
+            if (sure) route_weights(s, p, mx, lane, my_e, route_bias_masks(p, my_e), idx_t, w_t);
+            mode = sure ? kDone : kAll;
         } else if (mode == kAttempt) {
             int j = at;
             for (unsigned m = mark; m; m &= m - 1) {

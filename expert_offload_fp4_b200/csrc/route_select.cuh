@@ -491,13 +491,16 @@ __device__ __noinline__ double route_first_values(const RouteScratch s, const Ro
 }
 
 // The true ranks of a close call, whose wanted logits in s.l are exact: the others are far enough
-// from any.  Returns the expert of rank `lane`.  inv: 1 / sum of exp(l - mx) with a bias, else 1.
+// from any.  Returns the expert of rank `lane`.  inv: 1 / sum of exp(l - mx) with a bias, else 1;
+// where inv itself is only known to a relative eps, two wanted experts whose order hangs on it
+// clear `sure`.
 __device__ __noinline__ int route_settle(const RouteScratch s, const RouteChoice& p, const RouteClose& close, double mx,
-                                         double inv, int lane) {
-    double v = close.c;
+                                         double inv, double eps, int lane, bool& sure) {
+    double v = close.c, score = 0.0;
     if (close.want) {
         const double l = s.l[close.e];
-        v = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv + (p.bias ? (double)__ldg(p.bias + close.e) : 0.0);
+        score = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv;
+        v = score + (p.bias ? (double)__ldg(p.bias + close.e) : 0.0);
     }
     const unsigned long long key = lane < close.n ? order_key(v) : 0;
     int rank = 0;
@@ -507,12 +510,18 @@ __device__ __noinline__ int route_settle(const RouteScratch s, const RouteChoice
         rank += kj > key || (kj == key && ej < close.e);
     }
     __syncwarp();
-    unsigned* order = s.key32;           // (done with by now)
-    if (lane < close.n && rank < p.k) order[rank] = close.e;
+    unsigned* order = s.key32;           // (done with by now) the lane of each rank
+    if (lane < close.n) order[rank] = lane;
     __syncwarp();
-    const int e = lane < p.k ? (int)order[lane] : 0;
+    const int here = lane < close.n ? (int)order[lane] : 0, next = lane + 1 < close.n ? (int)order[lane + 1] : 0;
     __syncwarp();
-    return e;
+    const double dv = __shfl_sync(0xffffffffu, v, here) - __shfl_sync(0xffffffffu, v, next);
+    const double ds = __shfl_sync(0xffffffffu, score, here) - __shfl_sync(0xffffffffu, score, next);
+    // (both read before the &: a lane may not skip the second exchange)
+    const int want_here = __shfl_sync(0xffffffffu, (int)close.want, here);
+    const int want_next = __shfl_sync(0xffffffffu, (int)close.want, next);
+    sure = !__any_sync(0xffffffffu, lane < p.k && lane + 1 < close.n && (want_here & want_next) && dv <= fabs(ds) * eps && (dv != 0.0 || ds != 0.0));
+    return __shfl_sync(0xffffffffu, close.e, here);
 }
 
 // The fp64 selection value of expert e from s.l[e].
