@@ -34,6 +34,7 @@
 // All waits are bounded; a timeout sets bit 16 of *status and the CTA carries on.
 #include "tcgen05.cuh"
 
+#include <mutex>
 #include <type_traits>
 
 namespace moe {
@@ -323,7 +324,9 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     if (C > 1) cluster_arrive();   // peers may write here once every CTA's barriers are set
     const uint32_t tbase = *tmem_slot;
     const uint32_t sf_base = tbase + 2 * 8 * Tp, sfb = sf_base + 16 * S;
-    pdl_trigger();
+    // The next kernel may launch now, unless it could take y for its bf16 x: the decode FFN reads
+    // its x before it waits for the kernel ahead of it
+    if (GATED || a.y_f32) pdl_trigger();
     if (warp == 0 && lane == 0) {
         // the first stages' codes, while the kernel before this one finishes
         int n = 0;
@@ -721,11 +724,22 @@ static int check_rows(const void* p, int type, long long ld, int width, int T, c
     return MOE_OK;
 }
 
+// Do the rows of two matrices share any byte?
+static bool rows_overlap(const void* a, int a_type, long long lda, int na, const void* b, int b_type, long long ldb, int nb,
+                         int T) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t a1 = a0 + ((T - 1) * lda + na) * (a_type == MOE_BF16 ? 2 : 4);
+    const uintptr_t b1 = b0 + ((T - 1) * ldb + nb) * (b_type == MOE_BF16 ? 2 : 4);
+    return a0 < b1 && b0 < a1;
+}
+
 struct LinDevice {
     int sms = 0;
     int smem = 0;                              // dynamic shared memory a block may take
     int clusters[8][kLinMaxCluster + 1] = {};  // co-resident clusters per kernel and cluster size
 };
+
+static std::mutex g_lin_mu;   // guards the entries below while they are filled
 
 template <int FMT, int GATED, int XF32>
 static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& m1, LinDevice& d, cudaStream_t s) {
@@ -733,6 +747,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     const int Tp = (a.T + 1) & ~1, KTall = (a.K + kLinKT - 1) / kLinKT;
     a.tiles = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
     int* active = d.clusters[FMT * 4 + GATED * 2 + XF32];
+    std::unique_lock<std::mutex> lock(g_lin_mu);
     if (!active[1]) {
         MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem));
         for (int C = kLinMaxCluster; C >= 1; C--) {
@@ -751,6 +766,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
             active[C] = n < 1 ? 1 : n;
         }
     }
+    lock.unlock();
     // Cluster size: the least of, in twentieths of a stage's 0.4 us, the stages of the busiest
     // CTA, the conversion of its part of x (0.15 a KiB of digits) and the exchange of each tile
     // (0.5).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9.
@@ -808,6 +824,7 @@ static LinDevice* lin_device(int& rc) {
     if (e != cudaSuccess) { rc = cuda_fail(e, "cudaGetDevice"); return nullptr; }
     if (dev < 0 || dev >= 64) { rc = fail(MOE_EINVAL, "fp4: device ordinal out of range"); return nullptr; }
     LinDevice& d = devs[dev];
+    std::lock_guard<std::mutex> lock(g_lin_mu);
     if (!d.sms) {
         int smem = 0, sms = 0;
         if ((e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
@@ -881,6 +898,10 @@ extern "C" int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type
     if (add && (rc = check_rows(add, y_type, ld_add, w->N, T, "add"))) return rc;
     if ((reinterpret_cast<uintptr_t>(x) & 15) || (T > 1 && (ldx * (x_type == MOE_BF16 ? 2 : 4)) % 16))
         return fail(MOE_EINVAL, "fp4 linear: rows of x must be 16-byte aligned");
+    if (rows_overlap(x, x_type, ldx, w->K, y, y_type, ldy, w->N, T))
+        return fail(MOE_EINVAL, "fp4 linear: y overlaps x");
+    if (add && !(add == y && (ld_add == ldy || T == 1)) && rows_overlap(add, y_type, ld_add, w->N, y, y_type, ldy, w->N, T))
+        return fail(MOE_EINVAL, "fp4 linear: y overlaps add (it may only be add itself)");
     LinArgs a{};
     a.T = T;
     a.x = x; a.x_f32 = x_type == MOE_F32; a.ldx = ldx;
@@ -902,6 +923,8 @@ extern "C" int moe_fp4_swiglu(const moe_fp4_weight* gate, const moe_fp4_weight* 
     if ((rc = check_rows(h, MOE_F32, ldh, gate->N, T, "h"))) return rc;
     if ((reinterpret_cast<uintptr_t>(x) & 15) || (T > 1 && (ldx * (x_type == MOE_BF16 ? 2 : 4)) % 16))
         return fail(MOE_EINVAL, "fp4 swiglu: rows of x must be 16-byte aligned");
+    if (rows_overlap(x, x_type, ldx, gate->K, h, MOE_F32, ldh, gate->N, T))
+        return fail(MOE_EINVAL, "fp4 swiglu: h overlaps x");
     LinArgs a{};
     a.T = T;
     a.x = x; a.x_f32 = x_type == MOE_F32; a.ldx = ldx;

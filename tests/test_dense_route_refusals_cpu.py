@@ -99,6 +99,12 @@ def test_fp4_calls_refuse_bad_arguments(m):
     linear(b"aligned", weight(codes=p + 4))
     linear(b"T must", T=0)
     linear(b"T must", T=17)
+    big = (C.c_uint8 * 4096)()
+    q = (C.addressof(big) + 15) // 16 * 16
+    linear(b"y overlaps x", x=q, y=q + 64)
+    linear(b"y overlaps x", x=q, y=q + 2 * 64 * 2 - 2)
+    linear(b"y overlaps add", x=q, y=q + 512, add=q + 512 + 2)
+    linear(b"y overlaps add", x=q, y=q + 512, add=q + 512, lda=66)
     linear(b"K too large", weight(K=131072 + 32), T=1, ldx=1 << 20)
     linear(b"K too large", weight(K=16416), T=15, ldx=1 << 20)
     linear(b"N too large", weight(N=(1 << 30) + 1))
@@ -120,6 +126,7 @@ def test_fp4_calls_refuse_bad_arguments(m):
         assert L.moe_fp4_swiglu(C.byref(g), C.byref(u), x, 0, ldx, T, h, ldh, st, None) == E.MOE_EINVAL
         assert expect in L.moe_last_error(), L.moe_last_error()
 
+    swiglu(b"h overlaps x", x=q, h=q + 128)
     swiglu(b"one shape", u=weight(N=65))
     swiglu(b"one shape", u=weight(K=96))
     swiglu(b"one shape", u=weight(fmt=E.MOE_MXFP4))
