@@ -25,7 +25,7 @@ class DecodeLayer:
             raise ValueError("T exceeds the pool's max_tokens")
         self.router = router
         self._options = None if router is None else asdict(router)
-        self._h = None       # the shared expert's hidden activations, grown as needed
+        self._h = []         # the shared expert's hidden activations: the last is the largest
         # overlap=False issues the miss copies before the FFN launch (the host waits
         # for the lookup first): slower, but safe under tools that serialise kernels
         self.pool, self.T, self.renormalize, self.overlap = pool, T, renormalize, overlap
@@ -71,9 +71,10 @@ class DecodeLayer:
         if shared.H != self.pool.H:
             raise ValueError("the shared expert's H differs from the pool's")
         # allocated before anything is launched: an FFN may be waiting for copies later
-        if self._h is None or self._h.numel() < self.T * shared.I:
-            self._h = torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device)
-        h = self._h[:self.T * shared.I].view(self.T, shared.I)
+        # (smaller ones stay: a call on another stream may still be using them)
+        if not self._h or self._h[-1].numel() < self.T * shared.I:
+            self._h.append(torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device))
+        h = self._h[-1][:self.T * shared.I].view(self.T, shared.I)
         self._routed(layer, x, wr, bias, stream)
         shared.add_to(x, h, self.y, self.status, stream)
         return self.y
