@@ -56,14 +56,23 @@ __device__ __forceinline__ void choose_row(L64 l64, bool rounded, uint8_t* scrat
     float mx;
     bool masked;
     RouteClose close;
-    const RouteStatus st = route_fast(s, p, delta, lane, mx, my_e, masked, close);
-    __syncwarp();
-    if (st == kRouteOpen) {
-        route_choose_exact(s, p, lane, idx_out, w_out);
-        return;
+    RouteStatus st;
+    unsigned groups = 0;
+    double inv = 1.0;
+    for (int i = 0;; i++) {
+        st = route_fast(s, p, delta, lane, groups, mx, my_e, masked, close);
+        __syncwarp();
+        if (st == kRouteCertain) break;
+        if (st == kRouteOpen || i == 2) {
+            route_choose_exact(s, p, lane, idx_out, w_out);
+            return;
+        }
+        if (!p.sigmoid && p.bias) inv = route_softmax_inv(s.l, p.E, mx, lane);
+        if (st == kRouteClose) break;
+        groups = route_settle_groups(s, p, close, mx, inv, lane);
+        close = RouteClose();
     }
     if (st == kRouteClose) {
-        const double inv = !p.sigmoid && p.bias ? route_softmax_inv(s.l, p.E, mx, lane) : 1.0;
         bool sure;
         my_e = route_settle(s, p, close, mx, inv, 0.0, lane, sure);
         masked = route_bias_masks(p, my_e);
@@ -425,6 +434,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
 enum ChooseMode {
     kDone,
     kRanks,      // exact logits of a few experts, then the order of their ranks
+    kGroups,     // exact logits of a few experts, then the groups they decide
     kAttempt,    // exact logits of the marked experts, then another route_attempt
     kAll         // every logit in fp64
 };
@@ -561,36 +571,45 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     }
     if (lane == 0) sh.w2[warp] = w2;
     __syncthreads();
+    bool choose = false;
+    unsigned groups = 0;
     if (t < g.T) {
         float wmax = 0.0f;
 #pragma unroll
         for (int i = 0; i < kGemmTokens; i++) wmax = !(sh.w2[i] <= wmax) ? sh.w2[i] : wmax;
         delta = (float)(1.02 * (kGemmError * sqrt((double)xn * (double)wmax) +
                                  0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
-        if (!(delta <= 0.05f)) {
-            mode = kAll;
-        } else {
+        if (!(delta <= 0.05f)) mode = kAll;
+        else choose = true;
+    }
+    while (true) {
+        if (choose) {
             bool masked;
-            const RouteStatus st = route_fast(s, p, delta, lane, mx, my_e, masked, close);
+            close = RouteClose();
+            const RouteStatus st = route_fast(s, p, delta, lane, groups, mx, my_e, masked, close);
             __syncwarp();
+            const bool common = !p.sigmoid && p.bias;     // the denominator hangs on every logit
             if (st == kRouteCertain) {
                 route_weights(s, p, mx, lane, my_e, masked, idx_t, w_t);
+                mode = kDone;
             } else if (st == kRouteClose) {
                 mode = kRanks;
-            } else if (!p.sigmoid && p.bias) {
-                mode = kAll;                 // the denominator hangs on every logit
+            } else if (common) {
+                mode = kAll;
+            } else if (st == kRouteGroups) {
+                mode = kGroups;
             } else {
                 eta = route_first_values(s, p, delta, lane, sm);
                 attempt();
             }
+            choose = false;
         }
-    }
-    while (__syncthreads_or(mode != kDone)) {
+        if (!__syncthreads_or(mode != kDone)) break;
         // publish what is wanted
         int n = mode == kAll ? p.E : 0, at = 0;      // at: this lane's first in the list
         if (mode == kAll && n <= 32) {
             if (lane < n) sh.want[warp][lane] = lane;
-        } else if (mode == kRanks) {
+        } else if (mode == kRanks || mode == kGroups) {
             const unsigned wants = __ballot_sync(0xffffffffu, close.want);
             n = __popc(wants);
             at = __popc(wants & ((1u << lane) - 1));
@@ -615,6 +634,12 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
             __syncwarp();
             route_choose_exact(s, p, lane, idx_t, w_t);
             mode = kDone;
+        } else if (mode == kGroups) {
+            if (close.want) s.l[close.e] = sh.got[warp][at];
+            __syncwarp();
+            groups = route_settle_groups(s, p, close, mx, 1.0, lane);
+            if (groups != 0) choose = true;
+            else mode = kAll;
         } else if (mode == kRanks) {
             if (close.want) s.l[close.e] = sh.got[warp][at];
             __syncwarp();

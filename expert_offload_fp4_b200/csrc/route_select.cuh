@@ -14,8 +14,13 @@
 // of all experts cost more than all the rest, so the choice is first made in fp32
 // (route_fast), with a bound eta on the values' error (eta also covers the error of
 // logits that come from the tensor cores), and stands if every distance that decided
-// it is above the bounds.  Else (route_attempt) values within their bounds of a
-// decision are computed again in fp64, and the choice is repeated until it stands.
+// it is above the bounds.  Groups or ranks that are closer are settled by the fp64 values
+// of the few experts they hang on (route_settle_groups, then route_fast again with the
+// groups given; route_settle).  What is left, such as more than 32 such experts, goes
+// through route_attempt: values within their bounds of a decision are computed again in
+// fp64, and the choice is repeated until it stands.  (With every close pair of groups
+// left to route_attempt, the few tokens that have one were a launch's tail: 16 tokens of
+// 4096 x 256 took 15.5 us, not 13.1, and 512 tokens 33.4, not 27.3.)
 //
 // b_e = -inf masks expert e (as l_e = -inf does): it adds nothing to its group,
 // ranks below every unmasked expert and weighs 0.  A NaN c ranks like a masked
@@ -90,12 +95,15 @@ constexpr unsigned kMaskedKey32 = 0x007fffffu;   // order_key32(-inf)
 enum RouteStatus {
     kRouteCertain,   // the choice stands
     kRouteClose,     // the groups stand, but some ranks are too close to call: see RouteClose
+    kRouteGroups,    // groups are too close to call: see RouteClose
     kRouteOpen       // left to the 64-bit way
 };
 
-// The ranks and the experts just below them, one a lane (lanes >= n: none).
+// The ranks and the experts just below them, one a lane (lanes >= n: none); or, where groups are
+// close, the experts that may count in one of those.
 struct RouteClose {
     int n = 0, e = 0;
+    unsigned kept = 0;   // the groups that are certainly kept, in route_fast's form
     float c = 0.0f;      // selection value (by_logit: the logit)
     bool want = false;   // it has to be known exactly
     bool by_logit = false;
@@ -146,10 +154,14 @@ struct RouteTop32 {
     }
 };
 
+// The lanes of a group, which find its largest values together: 2^route_group_shift.
+__device__ __forceinline__ int route_group_shift(int n_group) { return 31 - __clz(32 / n_group); }
+
 // The choice from the fp32 logits, each within delta of its logit.  If it is certain, my_e is
 // the expert of rank `lane` (masked: chosen for want of others); mx: the largest logit.
-__device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const RouteChoice& p, float delta, int lane, float& mx,
-                                                  int& my_e, bool& masked, RouteClose& close_out) {
+// groups: 0, or the groups to keep (bit: each one's first lane).
+__device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const RouteChoice& p, float delta, int lane,
+                                                  unsigned groups, float& mx, int& my_e, bool& masked, RouteClose& close_out) {
     const float* sl = s.l32;
     unsigned* sk = s.key32;
     bool odd = delta > 0.05f;              // also NaN and infinities: left to the 64-bit way
@@ -206,10 +218,10 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
     if (grouped) {
         // 2^x lanes per group find its two largest; then the groups are chosen like experts
         const int gs = p.E / p.n_group;
-        const int sh = 31 - __clz(32 / p.n_group), per = 1 << sh;
+        const int sh = route_group_shift(p.n_group), per = 1 << sh;
         const int g = lane >> sh, r = lane & (per - 1);
         unsigned a = 0, b = 0;
-        if (g < p.n_group) {
+        if (g < p.n_group && groups == 0) {
 #pragma unroll 2
             for (int e = r; e < gs; e += per) {
                 const unsigned v = sk[g * gs + e];
@@ -235,8 +247,32 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
             if ((win & -win) >> lane & 1u) left = 0;
         }
         const unsigned next = __reduce_max_sync(0xffffffffu, left);
-        // (equal exact logits are a tie, which the lower group has won)
-        if (eta > 0.0f && key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta) return kRouteOpen;
+        if (groups) {
+            kept = groups;
+        } else if (eta > 0.0f && key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta) {
+            // The groups that could change places over the boundary, and their experts that could
+            // be among the ones that count
+            const float tol = 2 * p.group_top * eta;
+            const bool in = (kept >> lane) & 1u;
+            const unsigned open = __ballot_sync(0xffffffffu, leader && (in ? G - key32_value(next) <= tol
+                                                                           : key32_value(lowest) - G <= tol));
+            const float floor = key32_value(p.group_top == 2 && b > kMaskedKey32 ? b : a) - 2 * eta;
+            int n = 0;
+            for (int i = 0; i < p.E; i += 32) {
+                const int at = i + lane, src = at < p.E ? (at / gs) << sh : 0;
+                const float low = __shfl_sync(0xffffffffu, floor, src);
+                const unsigned v = at < p.E ? sk[at] : 0;
+                unsigned h = __ballot_sync(0xffffffffu, ((open >> src) & 1u) && v > kMaskedKey32 && key32_value(v) >= low);
+                for (; h; h &= h - 1, n++)
+                    if (lane == n) close_out.e = i + __ffs(h) - 1;
+            }
+            if (n > 32) return kRouteOpen;
+            close_out.n = n;
+            close_out.kept = kept & ~open;
+            close_out.want = lane < n;
+            close_out.by_logit = by_logit;
+            return kRouteGroups;
+        }
         // take the other groups out
         if (g < p.n_group && !((kept >> (g << sh)) & 1u))
             for (int e = r; e < gs; e += per) sk[g * gs + e] = 0;
@@ -522,6 +558,45 @@ __device__ __noinline__ int route_settle(const RouteScratch s, const RouteChoice
     const int want_next = __shfl_sync(0xffffffffu, (int)close.want, next);
     sure = !__any_sync(0xffffffffu, lane < p.k && lane + 1 < close.n && (want_here & want_next) && dv <= fabs(ds) * eps && (dv != 0.0 || ds != 0.0));
     return __shfl_sync(0xffffffffu, close.e, here);
+}
+
+// The groups to keep where some were close, from the exact logits of the wanted experts; in
+// route_fast's form.  inv: as for route_settle.
+__device__ __noinline__ unsigned route_settle_groups(const RouteScratch s, const RouteChoice& p, const RouteClose& close, double mx,
+                                                     double inv, int lane) {
+    const int gs = p.E / p.n_group, g = close.want ? close.e / gs : -1;
+    double v = 0.0;
+    if (close.want) {
+        const double l = s.l[close.e];
+        v = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv;
+        v += p.bias ? (double)__ldg(p.bias + close.e) : 0.0;
+    }
+    // each group's best (its lane stands for the group) and second best
+    int above = 0;
+    bool two = false;
+    double second = 0.0;
+    for (int j = 0; j < close.n; j++) {
+        const double vj = __shfl_sync(0xffffffffu, v, j);
+        const int gj = __shfl_sync(0xffffffffu, g, j);
+        const bool mine = gj == g && j != lane, over = vj > v || (vj == v && j < lane);
+        above += mine && over;
+        if (mine && !over) {
+            second = two ? fmax(second, vj) : vj;
+            two = true;
+        }
+    }
+    const int best = close.want && above == 0;
+    const double G = p.group_top == 2 && two ? v + second : v;
+    // the best of them take the places that are left; equal ones: the lower
+    int better = 0;
+    for (int j = 0; j < close.n; j++) {
+        const double Gj = __shfl_sync(0xffffffffu, G, j);
+        const int gj = __shfl_sync(0xffffffffu, g, j);
+        const int bj = __shfl_sync(0xffffffffu, best, j);
+        better += bj && (Gj > G || (Gj == G && gj < g));
+    }
+    const bool keep = best && better < p.topk_group - __popc(close.kept);
+    return close.kept | __reduce_or_sync(0xffffffffu, keep ? 1u << (g << route_group_shift(p.n_group)) : 0u);
 }
 
 // The fp64 selection value of expert e from s.l[e].

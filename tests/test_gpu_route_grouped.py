@@ -94,6 +94,77 @@ def test_choice_between_experts_that_fp32_sums_cannot_tell_apart(m, T):
         check_grouped(x, wr, None, k, run_grouped(m, x, wr, None, k, **opt), **opt)
 
 
+# near: groups that are near-copies of group 0 (the rest are independent), one of them an exact copy
+CLOSE_GROUPS = [
+    # E, n_group, topk_group, group_top, near, score, with_bias
+    (256, 8, 4, 2, 5, "sigmoid", True),
+    (256, 8, 4, 2, 8, "sigmoid", True),
+    (128, 8, 3, 1, 4, "softmax", False),
+    (96, 4, 2, 2, 3, "softmax", False),
+    (160, 32, 20, 2, 32, "sigmoid", False),
+    (64, 4, 1, 1, 4, "sigmoid", True),
+    (48, 3, 2, 2, 3, "softmax", True),
+    (12, 6, 3, 2, 6, "softmax", True),
+]
+
+
+def near_copies(rows, gs, near, rng, step, share):
+    """rows [E, n] with groups 1 .. near - 1 replaced by group 0 with a share of its elements changed
+    by step(values), the last of them left equal to it."""
+    for g in range(1, near):
+        part = rows[:gs].copy()
+        if g + 1 < near:
+            hit = rng.random(part.shape) < share
+            part[hit] = step(part[hit])
+        rows[g * gs:(g + 1) * gs] = part
+    return rows
+
+
+@pytest.mark.parametrize("T", [1, 9, 16, 40, 700])
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,near,score,with_bias", CLOSE_GROUPS)
+def test_choice_between_groups_that_fp32_sums_cannot_tell_apart(m, T, E, n_group, topk_group, group_top, near, score, with_bias):
+    H, gs, rng = 512, E // n_group, np.random.default_rng(T + E)
+    x, wr, b = inputs(T, H, E, 31 * T + E)
+    # a neighbouring bf16 value: 2^-8 of an element
+    step = lambda v: (v.view(np.uint32) + np.uint32(0x10000)).view(np.float32)
+    wr = torch.from_numpy(near_copies(wr.float().numpy().copy(), gs, near, rng, step, 0.02)).bfloat16()
+    if with_bias:
+        b = torch.from_numpy(near_copies(b.numpy().copy()[:, None], gs, near, rng, lambda v: v + np.float32(1e-6), 0.3)[:, 0].copy())
+    else:
+        b = None
+    k = min(8, topk_group * gs)
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+    got = run_grouped(m, x, wr, b, k, **kw)
+    # (expert by expert in one order, so that equal rows have equal logits)
+    xd, wd = x.double().numpy(), wr.double().numpy()
+    logits = np.stack([(xd * row).sum(1) for row in wd], 1)
+    ri, rw = choose(logits, k, bias=None if b is None else b.numpy(), **kw)
+    assert np.array_equal(got[0], ri)
+    dl = 2.0 ** -17 * np.linalg.norm(xd, axis=1)[:, None] * np.linalg.norm(wd, axis=1).max()
+    assert np.all(np.abs(got[1] - rw) <= rw * (4 * dl + 2.0 ** -24) + 1e-45)
+
+
+@pytest.mark.parametrize("T", [1, 333])
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,near,score,with_bias", CLOSE_GROUPS)
+def test_select_between_close_groups(m, T, E, n_group, topk_group, group_top, near, score, with_bias):
+    gs, rng = E // n_group, np.random.default_rng(T + E)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    step = lambda v: np.nextafter(v, np.float32(9.0))
+    for t in range(T):
+        near_copies(l[t][:, None], gs, near, rng, step, 0.5)
+    b = None
+    if with_bias:
+        b = near_copies(((rng.random(E, np.float32) - 0.5) * 0.2)[:, None], gs, near, rng, step, 0.5)[:, 0].copy()
+    k = min(8, topk_group * gs)
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), float("nan"), device="cuda")
+    m.route_select(torch.from_numpy(l).cuda(), idx, w, bias=None if b is None else torch.from_numpy(b).cuda(), **kw)
+    ri, rw = choose(l.astype(np.float64), k, bias=b, **kw)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.all(np.abs(w.cpu().numpy() - rw) <= rw * 2.0 ** -23 + 1e-45)
+
+
 @pytest.mark.parametrize("T", [1, 5, 140])
 def test_equal_experts_and_zero_tokens_go_to_the_lower_index(m, T):
     x, wr, _ = inputs(T, 256, 32, 5)
