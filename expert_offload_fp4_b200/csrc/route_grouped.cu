@@ -533,23 +533,10 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
         if (lane < g.split) xn = __ldg(g.xn + (size_t)lane * g.T + t);
         // (the sum over the tiles of experts is more than their largest)
         for (int c = lane; c < g.split * g.n_tiles; c += 32) xm += __ldg(g.xm + (size_t)c * g.T + t);
-#pragma unroll 1
-        for (int e = 4 * lane; e < p.E; e += 128) {
-            const float* col = g.part + (size_t)t * g.Ep + e;      // (rows are padded to 32)
-            float bias[4], l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto put = [&](int e, const float (&l)[4]) {
+            float bias[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) bias[i] = p.bias && e + i < p.E ? __ldg(p.bias + e + i) : 0.0f;
-            for (int c0 = 0; c0 < g.split; c0 += 8) {
-                float4 v[8];
-#pragma unroll
-                for (int c = 0; c < 8; c++)
-                    v[c] = c0 + c < g.split ? __ldg(reinterpret_cast<const float4*>(col + (size_t)(c0 + c) * g.T * g.Ep))
-                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    l[0] += v[c].x; l[1] += v[c].y; l[2] += v[c].z; l[3] += v[c].w;
-                }
-            }
             if (p.E % 4 == 0) {     // four at once: a quarter of the shared-memory conflicts
                 *reinterpret_cast<double2*>(s.l + e) = make_double2(l[0], l[1]);
                 *reinterpret_cast<double2*>(s.l + e + 2) = make_double2(l[2], l[3]);
@@ -560,6 +547,31 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
                 for (int i = 0; i < 4; i++)
                     if (e + i < p.E) s.fill(e + i, l[i], l[i], bias[i]);
             }
+        };
+        // two times 128 experts, eight parts of each on their way together
+#pragma unroll 1
+        for (int e = 4 * lane; e < p.E; e += 256) {
+            const float* col = g.part + (size_t)t * g.Ep + e;      // (rows are padded to 32)
+            const bool two = e + 128 < p.E;
+            float l[2][4] = {};
+            for (int c0 = 0; c0 < g.split; c0 += 8) {
+                float4 v[2][8];
+#pragma unroll
+                for (int c = 0; c < 8; c++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        v[h][c] = c0 + c < g.split && (h == 0 || two)
+                                      ? __ldg(reinterpret_cast<const float4*>(col + (size_t)(c0 + c) * g.T * g.Ep + 128 * h))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 8; c++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        l[h][0] += v[h][c].x; l[h][1] += v[h][c].y; l[h][2] += v[h][c].z; l[h][3] += v[h][c].w;
+                    }
+            }
+            put(e, l[0]);
+            if (two) put(e + 128, l[1]);
         }
     }
 #pragma unroll
