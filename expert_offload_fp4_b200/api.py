@@ -218,7 +218,7 @@ def route_grouped(x, wr, idx, w, workspace, *, score="sigmoid", bias=None, n_gro
     not enter the weights; -inf masks an expert) within the topk_group best of n_group
     groups, a group counting its group_top (1 or 2) best; w = scale * score, over the
     chosen scores' sum if renormalize.  workspace: route_grouped_workspace_bytes(T, E)
-    bytes, zeroed before its first use."""
+    bytes (enough for fewer tokens, too), zeroed before its first use."""
     _need(x.dim() == 2 and wr.dim() == 2 and x.dtype == wr.dtype == torch.bfloat16 and x.shape[1] == wr.shape[1]
           and x.is_contiguous() and wr.is_contiguous(), "x [T, H] and wr [E, H] must be contiguous bfloat16")
     T, H = x.shape

@@ -1,15 +1,21 @@
 // Grouped router: logits x W_r^T, then the choice of route_select.cuh.
 //
 // Few tokens (a decode step): the logits are fp64 sums of exact products, on the CUDA
-// cores.  Two experts a CTA, four warps each, so that the few hundred rows of W_r are
-// read by every SM at once; the last CTA of a token tile (a ticket per tile, reset by
-// that CTA) makes the choice, one warp a token.
+// cores.  Two experts a CTA, its eight warps over parts of H, so that the few hundred rows
+// of W_r are read by every SM at once; the last CTA of a token tile (a ticket per tile,
+// reset by that CTA) makes the choice, one warp a token.  Latency: for one token of 4096 x 256,
+// 8.5 us (launch and products 2.7, the choice 5.5), which is 2.1 MB at 0.25 TB/s.
 //
 // Many tokens (a prompt): fp64 would take 100 times the tensor cores' time.  A tcgen05
 // GEMM gives the logits in fp32 together with |x_t| and |W_e|, from which a bound on
 // a logit's error follows; the choice then computes a logit again in fp64, from x and
 // W_r, only where a decision hangs on less than that bound allows (a few tokens in a
-// hundred, a few experts each).  So both ways choose the same experts.
+// hundred, a few experts each).  So both ways choose the same experts.  8192 tokens of
+// 4096 x 256 take 70 us: the GEMM 23 (17 GFLOP, 0.75 PFLOP/s; its accumulators are read out
+// every 128 of H), the choice 42 (some 2400 instructions a token).  The GEMM's fixed cost
+// makes it the slower way up to 32 tokens: 24 tokens of 4096 x 256 take 18.6 us in fp64 and
+// 20.1 with it, 32 of 2048 x 128 10.2 and 13.3, 32 of 7168 x 256 26.6 and 27.6; 40 tokens
+// 23.7 and 21.6, 12.5 and 13.3, 34.9 and 27.9.
 #include "tcgen05.cuh"
 #include "route_select.cuh"
 
@@ -21,7 +27,7 @@ int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_
 constexpr int kChooseWarps = 8;          // warps per CTA of the kernels for few tokens and given logits
 constexpr int kGemmTokens = 4;           // tokens, a warp each, per CTA of the choice after the GEMM
 constexpr int kSmallTile = 8;            // largest token tile of the fp64 kernel
-constexpr int kSmallT = 16;              // most tokens it takes
+constexpr int kSmallT = 32;              // most tokens it takes
 constexpr size_t kCounterBytes = 256;    // its tickets, at the start of the workspace
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
@@ -826,12 +832,20 @@ int preload_route_grouped_kernels() {
 
 using namespace moe;
 
-extern "C" size_t moe_route_grouped_workspace_bytes(int T, int E) {
-    if (T <= 0 || E <= 0 || E > kMaxE) return 0;
+// What a call with T tokens uses.
+static size_t route_workspace(int T, int E) {
     if (T <= kSmallT) return kCounterBytes + up256(size_t(T) * E * sizeof(double));
     const size_t split = route_split(T, E), Ep = (E + 31) / 32 * 32;
     const size_t tiles = (E + kRgMaxN - 1) / kRgMaxN;
     return kCounterBytes + up256(split * T * Ep * 4) + up256(split * T * 4) + up256(split * tiles * T * 4) + up256(size_t(E) * 4);
+}
+
+extern "C" size_t moe_route_grouped_workspace_bytes(int T, int E) {
+    if (T <= 0 || E <= 0 || E > kMaxE) return 0;
+    // more tiles of tokens have fewer parts: the most of any number of tiles up to T's
+    size_t most = route_workspace(T, E);
+    for (int t = 128; t < T && t <= 128 * kRgTargetCtas; t += 128) most = std::max(most, route_workspace(t, E));
+    return most;
 }
 
 extern "C" int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H, int E,
@@ -844,7 +858,7 @@ extern "C" int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const 
     if (H <= 0 || H % 8) return fail(MOE_EINVAL, "grouped route: H must be a positive multiple of 8");
     if ((reinterpret_cast<uintptr_t>(x_bf16) | reinterpret_cast<uintptr_t>(wr_bf16)) & 15)
         return fail(MOE_EINVAL, "grouped route: x and W_r must be 16-byte aligned");
-    if (!workspace || workspace_bytes < moe_route_grouped_workspace_bytes(T, E))
+    if (!workspace || workspace_bytes < route_workspace(T, E))
         return fail(MOE_EINVAL, "grouped route: workspace missing or smaller than moe_route_grouped_workspace_bytes");
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_EINVAL, "grouped route: workspace must be 256-byte aligned");
     const RouteCall r{(const uint16_t*)x_bf16, (const uint16_t*)wr_bf16, T, H, p, idx, w, (char*)workspace, (cudaStream_t)stream};

@@ -249,9 +249,10 @@ int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias
  * scores sum to 0 the renormalised weights are 0.  idx is always within [0, E).
  * x [T, H] and W_r [E, H] bf16, 16-byte aligned rows (H % 8 == 0); outputs idx
  * [T, k] int32 and w [T, k] fp32 in rank order.  workspace: device scratch of
- * moe_route_grouped_workspace_bytes(T, E) bytes, 256-byte aligned, zeroed before its
- * first use (every call leaves its counters, the first 256 bytes, zero); calls that may overlap, and
- * captured graphs that may be replayed at the same time, need one each.  E <= 1024.
+ * moe_route_grouped_workspace_bytes(T, E) bytes (enough for fewer tokens, too), 256-byte
+ * aligned, zeroed before its first use (every call leaves its counters, the first 256
+ * bytes, zero); calls that may overlap, and captured graphs that may be replayed at the
+ * same time, need one each.  E <= 1024.
  * Errors: MOE_EINVAL. */
 size_t moe_route_grouped_workspace_bytes(int T, int E);
 int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H, int E,
@@ -273,7 +274,9 @@ int moe_route_select(const void* logits, int type, long long ld, const float* bi
  * input); row strides ldx, ld_add, ldy in elements.  Sums in fp32, one rounding to
  * y_type at the end; x enters to 2^-22 of its largest element in the token (bf16
  * elements down to 2^-14 of it exactly).  A NaN or infinite element makes all of
- * its token's outputs NaN.  T from 1 to 16; K * T (K rounded up to 256, T to even) at most 262144.
+ * its token's outputs NaN; so may weights so large (MXFP4 scales above 2^96) that
+ * 4 sum_k |W[n, k]| / S leaves fp32's range.  T from 1 to 16; K * T (K rounded up to
+ * 256, T to even) at most 262144.
  * Bounded device waits set bit 16 of *status (device int, caller-zeroed) on timeout.
  * Errors: MOE_EINVAL. */
 int moe_fp4_linear(const moe_fp4_weight* w, const void* x, int x_type, long long ldx, int T, const void* add,

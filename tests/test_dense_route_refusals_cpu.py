@@ -201,3 +201,11 @@ def test_shared_expert_and_routed_layer_refusals(m):
     assert call(None, None, s1) == E.MOE_EINVAL and b"null pool" in L.moe_last_error()
     assert call(p, s1, s1) == E.MOE_EINVAL and b"copy_stream" in L.moe_last_error()
     assert call(p, s1, None) == E.MOE_EINVAL and b"copy_stream" in L.moe_last_error()
+
+
+@pytest.mark.parametrize("E", [1, 64, 160, 300, 1024])
+def test_grouped_workspace_serves_fewer_tokens(E):
+    from expert_offload_fp4_b200 import _lib
+    size = _lib.load().moe_route_grouped_workspace_bytes
+    sizes = [size(T, E) for T in [*range(1, 300), *range(300, 25000, 97)]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
