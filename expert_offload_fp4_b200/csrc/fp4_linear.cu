@@ -769,7 +769,9 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     lock.unlock();
     // Cluster size: the least of, in twentieths of a stage's 0.4 us, the stages of the busiest
     // CTA, the conversion of its part of x (0.15 a KiB of digits) and the exchange of each tile
-    // (0.5).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9.
+    // (0.3).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9; an
+    // exchange of 0.5 has one CTA a tile at 131072 x 4096 for one token: 56.4 us, not 51.3.  Over
+    // 120 sizes the choice is 1.1 % above the best C on average, 11 % at most.
     // At most 128 KiB of digits, so that four stages fit beside them
     int bestC = 0;
     long long best = 0;
@@ -778,7 +780,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
         if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
         if (4 * Tp * kt * kLinKT > 128 * 1024) continue;
         const int ncl = std::min(a.tiles, active[C]), rounds = (a.tiles + ncl - 1) / ncl;
-        const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 10 * rounds;
+        const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 6 * rounds;
         if (!bestC || cost < best) { best = cost; bestC = C; }
     }
     if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
