@@ -162,6 +162,39 @@ def test_result_does_not_depend_on_the_other_tokens_and_repeats(m):
     assert torch.equal(whole, run_linear(m, x, Wq, torch.float32))
 
 
+@pytest.mark.parametrize("T", [1, 5])
+def test_codes_beyond_32_bit_offsets(m, T):
+    """4.3 GB of codes; rows spread over them, the last ones included."""
+    N, K, yd = 2 ** 20 + 77, 8192, torch.float32
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(0x20, 0x50, (N, K // 16), dtype=torch.uint8, device="cuda")
+    x = acts(T, K, torch.bfloat16, 40)
+    got = run_linear(m, x, m.FP4Weight(codes, scales, "nvfp4", 0.75), yd).double().numpy()
+    rows = torch.cat([torch.arange(0, N, 20011), torch.arange(N - 80, N)])
+    at = rows.cuda()
+    W = oracle.dequant("nvfp4", codes[at].cpu().numpy(), scales[at].cpu().numpy(), 1.0).astype(np.float64) * 0.75
+    ref = x.double().numpy() @ W.T
+    assert np.all(np.abs(got[:, rows.numpy()] - ref) <= bound(x, W, K, yd, ref))
+    assert np.all(np.isfinite(got))
+
+
+def test_calls_on_two_streams_at_once(m):
+    mats = [weight(m, 4000, 1024, "nvfp4", 50)[0], weight(m, 3001, 2048, "mxfp4", 51)[0]]
+    xs = [acts(4, Wq.K, torch.bfloat16, 52 + i).cuda() for i, Wq in enumerate(mats)]
+    alone = [run_linear(m, x, Wq, torch.float32) for x, Wq in zip(xs, mats)]
+    streams = [torch.cuda.Stream() for _ in mats]
+    ys = [torch.empty((20, 4, Wq.N), device="cuda") for Wq in mats]
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for r in range(20):
+        for i, s in enumerate(streams):
+            m.fp4_linear(xs[i], mats[i], ys[i][r], st[i:i + 1], stream=s)
+    torch.cuda.synchronize()
+    assert not st.any()
+    for i in range(2):
+        assert all(torch.equal(y.cpu(), alone[i]) for y in ys[i])
+
+
 # ------------------------------------------------------------------ the gated pair
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])

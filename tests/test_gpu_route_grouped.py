@@ -224,6 +224,33 @@ def test_choice_does_not_depend_on_the_batch(m):
         assert np.array_equal(part[0], whole[0][lo:hi])
 
 
+@pytest.mark.parametrize("T", [3, 32, 90])
+def test_calls_on_two_streams_at_once(m, T):
+    kw = dict(n_group=8, topk_group=4, group_top=2)
+    cases = [inputs(T, 1024, 128, 60 + i) for i in range(2)]
+    alone = [run_grouped(m, x, wr, b, 6, **kw) for x, wr, b in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    on = [[t.cuda() for t in c] for c in cases]
+    ws = [torch.zeros(m.route_grouped_workspace_bytes(T, 128), dtype=torch.uint8, device="cuda") for _ in cases]
+    idx = torch.zeros((2, 20, T, 6), dtype=torch.int32, device="cuda")
+    w = torch.zeros((2, 20, T, 6), device="cuda")
+    torch.cuda.synchronize()
+    for r in range(20):
+        for i, s in enumerate(streams):
+            m.route_grouped(on[i][0], on[i][1], idx[i, r], w[i, r], ws[i], bias=on[i][2], stream=s, **kw)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(np.array_equal(a, alone[i][0]) for a in idx[i].cpu().numpy())
+        assert all(np.array_equal(a, alone[i][1]) for a in w[i].cpu().numpy())
+
+
+@pytest.mark.parametrize("T", [33, 129])
+@pytest.mark.parametrize("H,E,k", [(8, 5, 2), (16, 1024, 32), (72, 33, 4), (200, 257, 9)])
+def test_short_rows_and_odd_expert_counts_of_a_prompt(m, T, H, E, k):
+    x, wr, b = inputs(T, H, E, H + E)
+    check_grouped(x, wr, b, k, run_grouped(m, x, wr, b, k))
+
+
 @pytest.mark.parametrize("T", [1, 40, 520])
 def test_workspace_is_left_ready_and_graphs_replay(m, T):
     x, wr, b = inputs(T, 1024, 128, 11)
