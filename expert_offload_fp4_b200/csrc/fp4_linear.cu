@@ -736,6 +736,7 @@ static bool rows_overlap(const void* a, int a_type, long long lda, int na, const
 struct LinDevice {
     int sms = 0;
     int smem = 0;                              // dynamic shared memory a block may take
+    int sm_smem = 0, reserved = 0;             // shared memory of an SM, and what each block takes besides
     int clusters[8][kLinMaxCluster + 1] = {};  // co-resident clusters per kernel and cluster size
 };
 
@@ -791,7 +792,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     const long long total = (long long)((a.tiles + ncl - 1) / ncl) * kt;
     a.stages = (int)std::min<long long>(kLinMaxStages, total);
     while (a.stages > 1 && LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024 > d.smem) a.stages--;
-    const int smem = LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024;
+    int smem = LinSmem(a.stages, Tp, a.Kc, a.C, GATED).total + 1024;
     if (smem > d.smem) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
     if (a.stages == 1 && total > 1) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
     const int R = ((GATED ? 64 : 128) + a.C - 1) / a.C;
@@ -800,6 +801,10 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     const int cols = 2 * 8 * Tp + 16 * a.stages + 4;
     a.tmem_cols = 32;
     while ((int)a.tmem_cols < cols) a.tmem_cols *= 2;
+    // A block takes as large a share of the SM's shared memory as of its 512 TMEM columns, so that
+    // blocks which are on an SM together all have their columns: else clusters of two calls
+    // (on two streams) could each hold columns that a block of the other waits for
+    smem = std::max(smem, (int)((long long)d.sm_smem * a.tmem_cols / 512) - d.reserved);
 
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(ncl * a.C);
@@ -829,7 +834,9 @@ static LinDevice* lin_device(int& rc) {
     std::lock_guard<std::mutex> lock(g_lin_mu);
     if (!d.sms) {
         int smem = 0, sms = 0;
-        if ((e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+        if ((e = cudaDeviceGetAttribute(&d.sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&d.reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
             (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) {
             rc = cuda_fail(e, "cudaDeviceGetAttribute");
             return nullptr;

@@ -178,12 +178,14 @@ def test_codes_beyond_32_bit_offsets(m, T):
     assert np.all(np.isfinite(got))
 
 
-def test_calls_on_two_streams_at_once(m):
-    mats = [weight(m, 4000, 1024, "nvfp4", 50)[0], weight(m, 3001, 2048, "mxfp4", 51)[0]]
-    xs = [acts(4, Wq.K, torch.bfloat16, 52 + i).cuda() for i, Wq in enumerate(mats)]
+@pytest.mark.parametrize("T,shapes", [(4, [(4000, 1024), (3001, 2048)]), (16, [(4096, 1024), (4096, 1024)]),
+                                      (16, [(2048, 512), (6000, 2048)]), (12, [(512, 2048), (512, 2048)])])
+def test_calls_on_two_streams_at_once(m, T, shapes):
+    mats = [weight(m, N, K, fmt, 50)[0] for (N, K), fmt in zip(shapes, ("nvfp4", "mxfp4"))]
+    xs = [acts(T, Wq.K, torch.bfloat16, 52 + i).cuda() for i, Wq in enumerate(mats)]
     alone = [run_linear(m, x, Wq, torch.float32) for x, Wq in zip(xs, mats)]
     streams = [torch.cuda.Stream() for _ in mats]
-    ys = [torch.empty((20, 4, Wq.N), device="cuda") for Wq in mats]
+    ys = [torch.empty((20, T, Wq.N), device="cuda") for Wq in mats]
     st = torch.zeros(2, dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     for r in range(20):
