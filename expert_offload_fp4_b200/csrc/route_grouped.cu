@@ -11,8 +11,8 @@
 // a logit's error follows; the choice then computes a logit again in fp64, from x and
 // W_r, only where a decision hangs on less than that bound allows (a few tokens in a
 // hundred, a few experts each).  So both ways choose the same experts.  8192 tokens of
-// 4096 x 256 take 70 us: the GEMM 23 (17 GFLOP, 0.75 PFLOP/s; its accumulators are read out
-// every 128 of H), the choice 42 (some 2400 instructions a token).  The GEMM's fixed cost
+// 4096 x 256 take 66.6 us: the GEMM 23 (17 GFLOP, 0.75 PFLOP/s; its accumulators are read
+// out every 128 of H), the choice 39 (some 2400 instructions a token).  The GEMM's fixed cost
 // makes it the slower way up to 32 tokens: 24 tokens of 4096 x 256 take 18.6 us in fp64 and
 // 20.1 with it, 32 of 2048 x 128 10.2 and 13.3, 32 of 7168 x 256 26.6 and 27.6; 40 tokens
 // 23.7 and 21.6, 12.5 and 13.3, 34.9 and 27.9.
@@ -502,8 +502,11 @@ __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, co
     __syncthreads();
 }
 
-// One warp per token.
-__global__ void __launch_bounds__(kGemmTokens * 32, 4)
+// One warp per token.  Five CTAs on an SM hold 96 registers a thread and spill a few, which pays
+// where there are many: 8192 tokens of 4096 x 256 take 66.5 us with five and 70.0 with four, but
+// 2048 of 2048 x 128 take 23.4 and 22.4.
+template <int kCtas>
+__global__ void __launch_bounds__(kGemmTokens * 32, kCtas)
 route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, RouteGemmArgs g, RouteChoice p,
                          int32_t* __restrict__ idx, float* __restrict__ wout) {
     extern __shared__ __align__(16) uint8_t sm_raw[];
@@ -785,16 +788,18 @@ static int launch_large(const RouteCall& r) {
     int rc;
     if ((rc = make_tmap_2d(&mx, r.x, size_t(r.H) * 2, r.T, size_t(r.H) * 2, 128, 128, true))) return rc;
     if ((rc = make_tmap_2d(&mw, r.wr, size_t(r.H) * 2, E, size_t(r.H) * 2, 128, g.N, true))) return rc;
-    static bool gdone[64] = {}, cdone[64] = {};
+    static bool gdone[64] = {}, cdone[2][64] = {};
     // (the sums leave through 2 x 128 half rows of 528 bytes)
     const int smem = std::max(kRgStages * (16384 + g.N * 128), 256 * 528) + 1024;
     MOE_CUDA_TRY(raise_smem(route_gemm_kernel, kRgStages * (16384 + kRgMaxN * 128) + 1024, gdone));
     const dim3 grid(((r.T + 127) / 128) * g.n_tiles * g.split);
     MOE_CUDA_TRY(launch_pdl(route_gemm_kernel, grid, dim3(kRgThreads), smem, r.s, mx, mw, g));
-    auto kern = route_gemm_choose_kernel;
-    MOE_CUDA_TRY(raise_smem(kern, (int)(kGemmTokens * RouteScratch::bytes(kMaxE)), cdone));
-    MOE_CUDA_TRY(launch_pdl(kern, dim3((r.T + kGemmTokens - 1) / kGemmTokens), dim3(kGemmTokens * 32),
-                            kGemmTokens * RouteScratch::bytes(E), r.s, r.x, r.wr, g, r.p, r.idx, r.w));
+    const int ctas = (r.T + kGemmTokens - 1) / kGemmTokens;
+    const bool many = ctas > 8 * kRgTargetCtas;            // more than two rounds of four an SM
+    auto kern = many ? route_gemm_choose_kernel<5> : route_gemm_choose_kernel<4>;
+    MOE_CUDA_TRY(raise_smem(kern, (int)(kGemmTokens * RouteScratch::bytes(kMaxE)), cdone[many]));
+    MOE_CUDA_TRY(launch_pdl(kern, dim3(ctas), dim3(kGemmTokens * 32), kGemmTokens * RouteScratch::bytes(E), r.s, r.x, r.wr,
+                            g, r.p, r.idx, r.w));
     return MOE_OK;
 }
 
@@ -823,7 +828,8 @@ int preload_route_grouped_kernels() {
     MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<4>));
     MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, grouped_small_kernel<8>));
     MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_kernel));
-    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_choose_kernel));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_choose_kernel<4>));
+    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_gemm_choose_kernel<5>));
     MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, route_select_kernel));
     return MOE_OK;
 }
