@@ -454,7 +454,9 @@ struct ChooseShared {
 };
 
 // The wanted logits of the CTA's tokens in fp64, by all warps: each takes an eighth of H,
-// four dot products at a time.  Values go to got, or to the token's scratch where all are wanted.
+// four dot products at a time, U pieces of 8 elements of each on their way together.  Values go to
+// got, or to the token's scratch where all are wanted.
+template <int U>
 __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, const uint16_t* x, const uint16_t* wr, int H, int E,
                                              int t0, int warp, int lane) {
     int total = 0;
@@ -471,21 +473,27 @@ __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, co
         }
         double acc[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 1
-        for (int c = warp * 32 + lane; c < H / 8; c += 32 * kGemmTokens) {
-            uint4 xq[4], wq[4];
+        for (int c = warp * 32 + lane; c < H / 8; c += 32 * kGemmTokens * U) {
+            uint4 xq[U][4], wq[U][4];
 #pragma unroll
-            for (int a = 0; a < 4; a++) {
-                xq[a] = __ldg(xr[a] + c);
-                wq[a] = __ldg(wrow[a] + c);
-            }
+            for (int u = 0; u < U; u++)
 #pragma unroll
-            for (int a = 0; a < 4; a++) {
-                float xf[8], wf[8];
-                unpack8(xq[a], xf);
-                unpack8(wq[a], wf);
+                for (int a = 0; a < 4; a++) {
+                    const int at = c + 32 * kGemmTokens * u;
+                    const bool in = u == 0 || at < H / 8;
+                    xq[u][a] = in ? __ldg(xr[a] + at) : make_uint4(0, 0, 0, 0);
+                    wq[u][a] = in ? __ldg(wrow[a] + at) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int r = 0; r < 8; r++) acc[a] = fma((double)xf[r], (double)wf[r], acc[a]);
-            }
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int a = 0; a < 4; a++) {
+                    float xf[8], wf[8];
+                    unpack8(xq[u][a], xf);
+                    unpack8(wq[u][a], wf);
+#pragma unroll
+                    for (int r = 0; r < 8; r++) acc[a] = fma((double)xf[r], (double)wf[r], acc[a]);
+                }
         }
         const double v = warp_sum_tokens<4>(acc, lane);
         if (lane % 8 == 0) sh.part[buf][warp][lane / 8] = v;
@@ -502,7 +510,8 @@ __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, co
     __syncthreads();
 }
 
-// One warp per token.  Five CTAs on an SM hold 96 registers a thread and spill a few, which pays
+// One warp per token.  Five CTAs on an SM leave 96 registers a thread (so exact_logits has half the
+// loads in flight: with as many it spills, and a softmax with a bias takes 403 us, not 331), which pays
 // where there are many: 8192 tokens of 4096 x 256 take 66.5 us with five and 70.0 with four, but
 // 2048 of 2048 x 128 take 23.4 and 22.4.
 template <int kCtas>
@@ -649,7 +658,7 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
         }
         if (lane == 0) sh.n[warp] = n;
         __syncthreads();
-        exact_logits(sh, sm_raw, x, wr, g.H, p.E, t0, warp, lane);
+        exact_logits<kCtas == 4 ? 2 : 1>(sh, sm_raw, x, wr, g.H, p.E, t0, warp, lane);
         if (mode == kAll) {
             if (n <= 32 && lane < n) s.l[lane] = sh.got[warp][lane];
             __syncwarp();
