@@ -328,9 +328,6 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
     if (C > 1) cluster_arrive();   // peers may write here once every CTA's barriers are set
     const uint32_t tbase = *tmem_slot;
     const uint32_t sf_base = tbase + 2 * 8 * Tp, sfb = sf_base + 16 * S;
-    // The next kernel may launch now, unless it could take y for its bf16 x: the decode FFN reads
-    // its x before it waits for the kernel ahead of it
-    if (GATED || a.y_f32) pdl_trigger();
     if (warp == 0 && lane == 0) {
         // the first stages' codes, while the kernel before this one finishes
         int n = 0;
@@ -347,6 +344,10 @@ fp4_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constan
                 prefetch_l2(a.m[which].scales + (size_t)n * (a.K / BS) + k0 / BS + o);
     }
     pdl_wait();
+    // The next kernel may launch now.  Not before the wait: the decode FFN reads its bf16 x before it
+    // waits for the kernel ahead of it, so that kernel may let it start only when every kernel before
+    // is complete.  And not at all where this one's own y could be that x
+    if (GATED || a.y_f32) pdl_trigger();
 
     if (warp == 0) {
         if (lane == 0) {

@@ -119,12 +119,12 @@ grouped_small_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict_
     const int t0 = blockIdx.y * TT, nt = min(TT, T - t0);
     const int e0 = blockIdx.x * 2, e1 = min(e0 + 1, p.E - 1);
     const int nch = H / 8;
-    pdl_trigger();
     for (int c = threadIdx.x; c < nch; c += kChooseWarps * 32) {
         prefetch_l2(wr + size_t(e0) * H + c * 8);
         prefetch_l2(wr + size_t(e1) * H + c * 8);
     }
     pdl_wait();
+    pdl_trigger();   // (after the wait: a kernel that this lets start may read what earlier ones wrote)
     double acc[2 * TT];
 #pragma unroll
     for (int t = 0; t < 2 * TT; t++) acc[t] = 0.0;
@@ -283,8 +283,8 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = tmem_slot;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
 
     // sums of squares of W_r: experts dealt out to the warps w of n a CTA
     auto w_norms = [&](int w, int n) {
@@ -525,8 +525,8 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     const RouteScratch s(sm_raw + warp * RouteScratch::bytes(p.E), p.E);
     int32_t* idx_t = idx + size_t(t) * p.k;
     float* w_t = wout + size_t(t) * p.k;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     int mode = kDone, my_e = 0;
     unsigned mark = 0;
     float delta = 0.0f, mx = 0.0f;
@@ -701,8 +701,8 @@ route_select_kernel(const void* __restrict__ logits, int is_bf16, long long ld, 
                     int32_t* __restrict__ idx, float* __restrict__ wout) {
     extern __shared__ __align__(16) uint8_t sm_raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const int t = blockIdx.x * kChooseWarps + warp;
     if (t >= T) return;
     const uint16_t* lh = reinterpret_cast<const uint16_t*>(logits) + t * ld;

@@ -1,0 +1,104 @@
+"""Products and routers between decode FFNs as a program chains them: results that pass from one
+kernel to another while the next is already starting, on other streams, in reused buffers."""
+import numpy as np
+import pytest
+import torch
+
+from synthetic import gen, workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    from expert_offload_fp4_b200 import build
+    build.build()
+    import expert_offload_fp4_b200 as mod
+    return mod
+
+
+def workload(H, I, E, k, L):
+    return W.Workload(name="chain", H=H, I=I, E=E, k=k, L=L, fmt=W.NVFP4, seed=33, batches=(1,), steps=4, zipf_s=0.0,
+                      weight_recipe="normal", exp_range=(-6, -2))
+
+
+def bf16(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def full_pool(m, w, T):
+    """A pool whose slots hold every expert of every layer, and a layer's buffers."""
+    pool = m.Pool(w.H, w.I, w.E, w.k, w.L, w.fmt, w.L * w.E, max_tokens=T)
+    for l in range(w.L):
+        for e in range(w.E):
+            pool.load_expert(l, e, gen.expert_weights(w, l, e))
+    lo = m.DecodeLayer(pool, T)
+    idx = torch.arange(w.E, dtype=torch.int32, device="cuda").view(-1, w.k)
+    slot = torch.empty_like(idx)
+    for l in range(w.L):
+        m.stream_misses(pool, l, m.slot_lookup(pool, l, idx, slot), lo.copy_stream)
+    torch.cuda.synchronize()
+    return pool, lo
+
+
+def matrix(m, rows, K, seed, sigma=0.05):
+    """A 4-bit matrix of about N(0, sigma) entries."""
+    rng = np.random.default_rng(seed)
+    codes = torch.from_numpy(rng.integers(0, 256, (rows, K // 2), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy(rng.integers(0x34, 0x3C, (rows, K // 16), dtype=np.uint8)).cuda()
+    return m.FP4Weight(codes, scales, "nvfp4", sigma / 2.99)
+
+
+@pytest.mark.parametrize("between", ["swiglu", "linear", "route_small", "route_large", "select"])
+def test_resident_layers_with_another_kernel_between(m, between):
+    """A layer's y is the next layer's x, with a kernel between them that does not write it: the next
+    layer's early read of x finds y complete, whatever the kernel between lets start when."""
+    T, w = 4, workload(512, 256, 16, 2, 2)
+    pool, lo = full_pool(m, w, T)
+    try:
+        wr = [bf16(gen.router_weight(w, l)) for l in range(2)]
+        gate, up, head = matrix(m, 64, w.H, 1), matrix(m, 64, w.H, 2), matrix(m, 48, w.H, 3)
+        h, logits = torch.empty((T, 64), device="cuda"), torch.empty((T, 48), device="cuda")
+        many = torch.randn((40, w.H), device="cuda").bfloat16()
+        n = 40 if between == "route_large" else T
+        idx, wt = torch.empty((n, 2), dtype=torch.int32, device="cuda"), torch.empty((n, 2), device="cuda")
+        ws = torch.zeros(m.route_grouped_workspace_bytes(40, w.E), dtype=torch.uint8, device="cuda")
+        given = torch.randn((T, w.E), device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def layer(l, x, y):
+            m.decode_resident(pool, l, x.view(1, T, w.H), [wr[l]], None, 1, lo.idx, lo.w, lo.slot_of, lo.y_part,
+                              y.view(1, T, w.H), st)
+
+        def kernel(y):
+            if between == "swiglu":
+                m.fp4_swiglu(y, gate, up, h, st)
+            elif between == "linear":
+                m.fp4_linear(y, head, logits, st)
+            elif between == "route_small":
+                m.route_grouped(y, wr[1], idx, wt, ws)
+            elif between == "route_large":
+                m.route_grouped(many, wr[1], idx, wt, ws)
+            else:
+                m.route_select(given, idx, wt)
+
+        xs = [bf16(gen.activations(w, 0, s, T)) for s in range(20)]
+        want = []
+        for x in xs:
+            y0, y1 = torch.empty_like(x), torch.empty_like(x)
+            layer(0, x, y0)
+            torch.cuda.synchronize()
+            layer(1, y0, y1)
+            torch.cuda.synchronize()
+            want.append(y1)
+        y0 = torch.zeros_like(xs[0])
+        got = [torch.empty_like(x) for x in xs]
+        for x, y1 in zip(xs, got):
+            layer(0, x, y0)
+            kernel(y0)
+            layer(1, y0, y1)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    finally:
+        pool.close()
