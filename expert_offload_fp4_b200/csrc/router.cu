@@ -27,7 +27,6 @@ router_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr,
     extern __shared__ float xs[];  // [TT][H] fp32
     __shared__ int s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_trigger();   // the slot lookup may launch now; it waits for this grid to finish
     const int t0 = blockIdx.y * TT;
     const int nt = min(TT, T - t0);
     const int e0 = (blockIdx.x * kRouterWarps + warp) * EPW;
@@ -51,6 +50,7 @@ router_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr,
     };
     load_batch(0);
     pdl_wait();      // x (and the buffers this kernel writes) belong to earlier kernels
+    pdl_trigger();   // the next kernel may launch: one that reads x before its own wait finds it complete
 
     for (int v = threadIdx.x; v < TT * H / 8; v += blockDim.x) {
         const int t = (v * 8) / H, h = v * 8 - t * H;

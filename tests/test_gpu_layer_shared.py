@@ -49,7 +49,7 @@ def matrix(m, rows, K, seed, sigma=0.05):
     return m.FP4Weight(codes, scales, "nvfp4", sigma / 2.99)
 
 
-@pytest.mark.parametrize("between", ["swiglu", "linear", "route_small", "route_large", "select"])
+@pytest.mark.parametrize("between", ["swiglu", "linear", "route", "route_small", "route_large", "select"])
 def test_resident_layers_with_another_kernel_between(m, between):
     """A layer's y is the next layer's x, with a kernel between them that does not write it: the next
     layer's early read of x finds y complete, whatever the kernel between lets start when."""
@@ -63,6 +63,7 @@ def test_resident_layers_with_another_kernel_between(m, between):
         n = 40 if between == "route_large" else T
         idx, wt = torch.empty((n, 2), dtype=torch.int32, device="cuda"), torch.empty((n, 2), device="cuda")
         ws = torch.zeros(m.route_grouped_workspace_bytes(40, w.E), dtype=torch.uint8, device="cuda")
+        ws0 = torch.zeros(m.route_workspace_bytes(T, w.E), dtype=torch.uint8, device="cuda")
         given = torch.randn((T, w.E), device="cuda")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
 
@@ -75,6 +76,8 @@ def test_resident_layers_with_another_kernel_between(m, between):
                 m.fp4_swiglu(y, gate, up, h, st)
             elif between == "linear":
                 m.fp4_linear(y, head, logits, st)
+            elif between == "route":
+                m.route(y, wr[1], None, 2, 1, idx, wt, ws0)
             elif between == "route_small":
                 m.route_grouped(y, wr[1], idx, wt, ws)
             elif between == "route_large":
