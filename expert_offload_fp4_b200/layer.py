@@ -71,9 +71,11 @@ class DecodeLayer:
         if shared.H != self.pool.H:
             raise ValueError("the shared expert's H differs from the pool's")
         # allocated before anything is launched: an FFN may be waiting for copies later
-        # (smaller ones stay: a call on another stream may still be using them)
+        # (smaller ones stay: a call on another stream may still be using them), and from the
+        # memory of the stream that uses it: a block of another stream's may still be written there
         if not self._h or self._h[-1].numel() < self.T * shared.I:
-            self._h.append(torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device))
+            with torch.cuda.stream(stream):
+                self._h.append(torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device))
         h = self._h[-1][:self.T * shared.I].view(self.T, shared.I)
         self._routed(layer, x, wr, bias, stream)
         shared.add_to(x, h, self.y, self.status, stream)

@@ -105,3 +105,38 @@ def test_resident_layers_with_another_kernel_between(m, between):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     finally:
         pool.close()
+
+
+def shared_expert(m, H, I, seed):
+    return m.SharedExpert(matrix(m, I, H, seed), matrix(m, I, H, seed + 1), matrix(m, H, I, seed + 2))
+
+
+def test_shared_expert_of_a_layer_on_another_stream(m):
+    """The scratch for h is allocated inside the call.  Memory that the current stream has freed but is
+    still to write belongs to that stream, not to the layer's."""
+    T, w, I = 4, workload(512, 256, 16, 2, 1), 4096
+    pool, lo = full_pool(m, w, T)
+    try:
+        sh, wr = shared_expert(m, w.H, I, 4), bf16(gen.router_weight(w, 0))
+        x = bf16(gen.activations(w, 0, 0, T))
+        want = lo(0, x, wr, None, shared=sh).clone()
+        torch.cuda.synchronize()
+        other = torch.cuda.Stream()
+        for i in range(3):
+            fresh = m.DecodeLayer(pool, T)
+            torch.cuda.synchronize()
+            # on the current stream: a long wait, then writes to blocks of h's size, which are free for
+            # later work of that stream from here on
+            old = [torch.empty(T * I, device="cuda") for _ in range(8)]
+            torch.cuda._sleep(20_000_000)
+            for t in old:
+                t.fill_(float("nan"))
+            at = {t.data_ptr() for t in old}
+            del old, t
+            got = fresh(0, x, wr, None, stream=other, shared=sh)
+            assert fresh._h[-1].data_ptr() not in at
+            other.synchronize()
+            torch.cuda.synchronize()
+            assert int(fresh.status.item()) == 0 and torch.equal(got, want)
+    finally:
+        pool.close()
