@@ -303,10 +303,18 @@ class SharedExpert:
         self.gate, self.up, self.down = gate, up, down
         self.I, self.H = gate.N, gate.K
 
+    def hidden(self, x, h, status, stream=None):
+        """h [T, I] fp32 = silu(x W_gate^T) * (x W_up^T) for x [T, H] bf16."""
+        fp4_swiglu(x, self.gate, self.up, h, status, stream=stream)
+
+    def add_down(self, h, y, status, stream=None):
+        """y [T, H] bf16 += h W_down^T."""
+        fp4_linear(h, self.down, y, status, add=y, stream=stream)
+
     def add_to(self, x, h, y, status, stream=None):
         """y [T, H] bf16 += the expert's output for x [T, H] bf16; h [T, I] fp32 scratch."""
-        fp4_swiglu(x, self.gate, self.up, h, status, stream=stream)
-        fp4_linear(h, self.down, y, status, add=y, stream=stream)
+        self.hidden(x, h, status, stream)
+        self.add_down(h, y, status, stream)
 
 
 class Lookup:

@@ -58,8 +58,8 @@ class DecodeLayer:
 
     def __call__(self, layer, x, wr, bias, stream=None, shared=None):
         """x [T, H] bf16, wr [E, H] bf16, bias [E] fp32 (or None), all on the device.
-        Returns y [T, H] bf16 (a buffer reused by the next call).  shared: an
-        api.SharedExpert whose output is added to the routed experts'.
+        Returns y [T, H] bf16 (a buffer reused by the next call, which may take it as x).
+        shared: an api.SharedExpert whose output is added to the routed experts'.
 
         Order: route, lookup, FFN and combine are enqueued back to back on the
         compute stream; then the host collects the lookup's miss list and drives
@@ -77,8 +77,10 @@ class DecodeLayer:
             with torch.cuda.stream(stream):
                 self._h.append(torch.empty(self.T * shared.I, dtype=torch.float32, device=self.y.device))
         h = self._h[-1][:self.T * shared.I].view(self.T, shared.I)
+        # x is read before the routed experts' y is written: x may be the buffer that the last call returned
+        shared.hidden(x, h, self.status, stream)
         self._routed(layer, x, wr, bias, stream)
-        shared.add_to(x, h, self.y, self.status, stream)
+        shared.add_down(h, self.y, self.status, stream)
         return self.y
 
     def _route(self, x, wr, bias, stream):

@@ -140,3 +140,31 @@ def test_shared_expert_of_a_layer_on_another_stream(m):
             assert int(fresh.status.item()) == 0 and torch.equal(got, want)
     finally:
         pool.close()
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("grouped", [True, False])
+def test_a_layer_takes_the_buffer_it_returned(m, native, grouped):
+    """y of one call as x of the next, with a shared expert: the same bits as from a copy of y."""
+    T, w = 4, workload(512, 256, 16, 2, 3)
+    pool, _ = full_pool(m, w, T)
+    try:
+        routing = m.GroupedRouting(n_group=4, topk_group=2, group_top=2) if grouped else None
+        lo = m.DecodeLayer(pool, T, router=routing)
+        if not native:
+            lo.ffn_events = []
+        sh, wr = shared_expert(m, w.H, 320, 7), [bf16(gen.router_weight(w, l)) for l in range(w.L)]
+        x = bf16(gen.activations(w, 0, 0, T))
+        want = [x]
+        for l in range(w.L):
+            want.append(lo(l, want[-1], wr[l], None, shared=sh).clone())
+            torch.cuda.synchronize()
+        y = x
+        for l in range(w.L):
+            y = lo(l, y, wr[l], None, shared=sh)
+            assert torch.equal(y, want[l + 1])
+        for l in range(w.L):
+            y = lo(l, x if l == 0 else y, wr[l], None, shared=sh)
+        assert torch.equal(y, want[-1]) and int(lo.status.item()) == 0
+    finally:
+        pool.close()
