@@ -436,6 +436,9 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
 
 // ---------------------------------------------------------------- many tokens: choice
 
+// The larger one; a NaN on either side stays.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return b > a || b != b ? b : a; }
+
 // What a warp's token still needs.
 enum ChooseMode {
     kDone,
@@ -544,8 +547,7 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     // the norms and largest sums, on their way while the logits are read
     float w2 = 0.0f, xn = 0.0f, xm = 0.0f;
     for (int e = threadIdx.x; e < p.E; e += kGemmTokens * 32) {
-        const float v = __ldg(g.wn + e);
-        w2 = !(v <= w2) ? v : w2;               // a NaN stays
+        w2 = max_or_nan(w2, __ldg(g.wn + e));
     }
     if (t < g.T) {
         if (lane < g.split) xn = __ldg(g.xn + (size_t)lane * g.T + t);
@@ -594,8 +596,7 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, w2, off);
-        w2 = !(o <= w2) ? o : w2;
+        w2 = max_or_nan(w2, __shfl_xor_sync(0xffffffffu, w2, off));
         xn += __shfl_xor_sync(0xffffffffu, xn, off);
         xm += __shfl_xor_sync(0xffffffffu, xm, off);
     }
@@ -606,7 +607,7 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     if (t < g.T) {
         float wmax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kGemmTokens; i++) wmax = !(sh.w2[i] <= wmax) ? sh.w2[i] : wmax;
+        for (int i = 0; i < kGemmTokens; i++) wmax = max_or_nan(wmax, sh.w2[i]);
         delta = (float)(1.02 * (kGemmError * sqrt((double)xn * (double)wmax) +
                                  0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
         if (!(delta <= 0.05f)) mode = kAll;
