@@ -24,8 +24,8 @@
 //
 // b_e = -inf masks expert e (as l_e = -inf does): it adds nothing to its group,
 // ranks below every unmasked expert and weighs 0.  A NaN c ranks like a masked
-// one and keeps its NaN weight.  A token without any finite score gets the first
-// experts and weights 0.
+// one and keeps its score's weight (NaN unless only b was).  A token whose experts are
+// all masked gets the first ones and weights 0.
 #pragma once
 
 #include "common.cuh"

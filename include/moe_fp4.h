@@ -245,8 +245,10 @@ int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias
  * values of the exact logits, so it does not depend on T or on the order of sums.
  * bias_e = -inf masks expert e: it adds nothing to its group's value, ranks below
  * every unmasked expert of the kept groups (then by index) and has weight 0.  A NaN
- * selection value ranks like a masked one and its weight is NaN.  Where the chosen
- * scores sum to 0 the renormalised weights are 0.  idx is always within [0, E).
+ * selection value ranks like a masked one; its weight is still that of its score, NaN
+ * for a NaN logit (and renormalised, so are its token's others), not for a NaN bias.
+ * Where the chosen scores sum to 0 the renormalised weights are 0.  idx is always
+ * within [0, E).
  * x [T, H] and W_r [E, H] bf16, 16-byte aligned rows (H % 8 == 0); outputs idx
  * [T, k] int32 and w [T, k] fp32 in rank order.  workspace: device scratch of
  * moe_route_grouped_workspace_bytes(T, E) bytes (enough for fewer tokens, too), 256-byte

@@ -63,3 +63,21 @@ def test_a_nan_row_does_not_hide_the_largest_row(m):
         gi, gw = grouped(m, x, w, None, 4, **kw)
         ri, rw = choose(x.double().numpy() @ w.double().numpy().T, 4, **kw)
         assert np.array_equal(gi, ri), nan
+
+
+@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_bias_ranks_last_and_keeps_the_score_as_weight(m, T, score):
+    g = torch.Generator().manual_seed(5)
+    x, wr = torch.randn((T, 256), generator=g).bfloat16(), (torch.randn((24, 256), generator=g) * 0.05).bfloat16()
+    b = (torch.rand(24, generator=g) - 0.5) * 0.2
+    b[[1, 2, 5, 6, 7]] = float("nan")
+    for kw in (dict(score=score), dict(score=score, n_group=4, topk_group=2, group_top=2, renormalize=False)):
+        k = 12
+        gi, gw = grouped(m, x, wr, b, k, **kw)
+        l = x.double().numpy() @ wr.double().numpy().T
+        ri, rw = choose(l, k, bias=b.numpy(), **kw)
+        assert np.array_equal(gi, ri)
+        # logits of more than 32 tokens: 2^-17 |x| |W_e|, four times that in a renormalised weight
+        dl = 2.0 ** -17 * np.linalg.norm(x.double().numpy(), axis=1)[:, None] * float(wr.double().norm(dim=1).max())
+        assert np.all(np.abs(gw - rw) <= rw * (4 * dl + 2.0 ** -23))
