@@ -201,12 +201,16 @@ constexpr int kRgMaxN = 256;             // experts per CTA
 constexpr int kRgTargetCtas = 148;
 constexpr int kRgChunk = 2;              // stages (64 elements each) the tensor core sums by itself
 
-// Error of the tensor core's sums over |x_t| |W_e|: every MMA step of 16 elements may cut the
-// accumulator by one unit in its 24th bit and as much again in lining up its products, 2^-23 of
-// its size, which |x| |W| of the chunk bounds; 8 steps a chunk, and the chunks' bounds add up to
-// 2^-20 |x| |W|.  (Measured per step: 2^-25.6 where all products are positive.)  The chunks are
-// added in fp32 registers: 2^-24 of the largest sum each.
-constexpr double kGemmError = 0x1p-20;
+// Error of the tensor core's sums over |x_t| |W_e|.  What an MMA step does here, seen by sums of
+// powers of two at every place: it cuts its 16 products and the accumulator towards zero at the 25th
+// binary place below the largest exponent among them, adds them, and cuts the sum to 24 bits.  Let M
+// bound the sizes of all partial sums of a chunk and of its products: |x| |W| of the chunk does.  The
+// largest term loses nothing, so a step loses less than 16 2^-25 M (the chunk's first 15 2^-25 M) and
+// 2^-23 M for the sum: (20 n - 1) 2^-25 M in the n = 8 steps of a chunk, and the chunks' bounds add up
+// to as much of |x| |W|.  (One product of 1 before 127 of just under 2^-24 comes within a fifth of it;
+// dense rows err by 2^-21.9 of |x| |W| where all products are positive, 2^-23.6 of random sign.)  The
+// chunks are added in fp32 registers: 2^-24 of the largest sum each.
+constexpr double kGemmError = (20 * 4 * kRgChunk - 1) * 0x1p-25;
 
 struct RouteGemmArgs {
     int T, H, E, Ep;          // Ep: row length of the partial logits

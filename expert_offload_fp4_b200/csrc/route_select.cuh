@@ -154,6 +154,67 @@ struct RouteTop32 {
     }
 };
 
+// An expert's own error, which may be far less than the bound for all: a sigmoid's goes with its slope
+// s (1 - s) (which changes by less than 6 % within delta <= 0.05), a softmax's with the score (2.3 delta of
+// the logits and the denominator, fp32's 2^-17 and that of the argument).  sk: the keys of the values.
+struct RouteErrors {
+    const float* sl;
+    const unsigned* sk;
+    float mx, inv, delta, cmax;
+    int sigmoid;
+    __device__ __forceinline__ float of(int e) const {
+        if (sigmoid) {
+            const float v = __fdividef(1.0f, 1.0f + __expf(-sl[e]));
+            return 1.06f * delta * (v * (1.0f - v)) + 0x1p-20f + cmax * 0x1p-22f;
+        }
+        const float d = mx - sl[e];
+        return (2.3f * delta + 0x1p-17f + d * 0x1p-22f) * __expf(-d) * inv + cmax * 0x1p-22f;
+    }
+};
+
+// Is the least that a kept group's value can be above the most that any other's can, by the experts' own
+// errors?  per lanes a group (r: which), as in route_fast; in: this leader's group is kept.
+__device__ __noinline__ bool route_groups_clear(const RouteErrors errors, int gs, bool any, int g, int r, int per, bool leader,
+                                                bool in, int group_top) {
+    float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {-INFINITY, -INFINITY};   // the two largest of either
+    if (any)
+        for (int e = g * gs + r; e < (g + 1) * gs; e += per) {
+            const unsigned q = errors.sk[e];
+            if (q <= kMaskedKey32) continue;
+            const float v = key32_value(q), own = errors.of(e);
+            hi[1] = fmaxf(hi[1], fminf(hi[0], v + own));
+            hi[0] = fmaxf(hi[0], v + own);
+            lo[1] = fmaxf(lo[1], fminf(lo[0], v - own));
+            lo[0] = fmaxf(lo[0], v - own);
+        }
+    for (int off = per / 2; off >= 1; off >>= 1) {
+        const float h0 = __shfl_xor_sync(0xffffffffu, hi[0], off), h1 = __shfl_xor_sync(0xffffffffu, hi[1], off);
+        const float l0 = __shfl_xor_sync(0xffffffffu, lo[0], off), l1 = __shfl_xor_sync(0xffffffffu, lo[1], off);
+        hi[1] = fmaxf(fmaxf(hi[1], h1), fminf(hi[0], h0));
+        hi[0] = fmaxf(hi[0], h0);
+        lo[1] = fmaxf(fmaxf(lo[1], l1), fminf(lo[0], l0));
+        lo[0] = fmaxf(lo[0], l0);
+    }
+    const bool two = group_top == 2 && lo[1] > -INFINITY;
+    const unsigned most = __reduce_max_sync(0xffffffffu, leader && !in ? order_key32(two ? hi[0] + hi[1] : hi[0]) : 0u);
+    const unsigned least = ~__reduce_max_sync(0xffffffffu, leader && in ? ~order_key32(two ? lo[0] + lo[1] : lo[0]) : 0u);
+    return least > most;
+}
+
+// Is every rank clear of the next (my_e, my_q: expert and key of rank `lane`), and the last of all that is
+// left, by the experts' own errors?
+__device__ __noinline__ bool route_ranks_clear(const RouteErrors errors, int E, int k, int lane, int my_e, unsigned my_q, float eta) {
+    const float c = key32_value(my_q), own = errors.of(my_e);
+    const float next_c = __shfl_down_sync(0xffffffffu, c, 1), next_own = __shfl_down_sync(0xffffffffu, own, 1);
+    bool near = lane < k - 1 && c - next_c <= own + next_own;
+    const float low = __shfl_sync(0xffffffffu, c - own, k - 1);
+    for (int e = lane; e < E; e += 32) {
+        const unsigned v = errors.sk[e];
+        if (v > kMaskedKey32 && key32_value(v) + eta >= low) near |= key32_value(v) + errors.of(e) >= low;
+    }
+    return !__any_sync(0xffffffffu, near);
+}
+
 // The lanes of a group, which find its largest values together: 2^route_group_shift.
 __device__ __forceinline__ int route_group_shift(int n_group) { return 31 - __clz(32 / n_group); }
 
@@ -214,6 +275,8 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
         eta = (p.sigmoid ? 0.26f * delta + 0x1p-20f : p.bias ? (2.3f * delta + 0x1p-17f) * inv : 1.1f * delta + 0x1p-19f) +
               cmax * 0x1p-22f;
     }
+    const RouteErrors errors{sl, sk, mx, inv, delta, cmax, p.sigmoid};
+    const bool sharp = p.sigmoid ? delta > 0.0f && !by_logit : p.bias != nullptr;   // an expert's own error may be less than eta
     __syncwarp();
     if (grouped) {
         // 2^x lanes per group find its two largest; then the groups are chosen like experts
@@ -247,9 +310,12 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
             if ((win & -win) >> lane & 1u) left = 0;
         }
         const unsigned next = __reduce_max_sync(0xffffffffu, left);
+        bool clear = groups != 0 || eta == 0.0f || !(key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta);
+        if (!clear && sharp)
+            clear = route_groups_clear(errors, gs, g < p.n_group, g, r, per, leader, (kept >> lane) & 1u, p.group_top);
         if (groups) {
             kept = groups;
-        } else if (eta > 0.0f && key32_value(lowest) - key32_value(next) <= 2 * p.group_top * eta) {
+        } else if (!clear) {
             // The groups that could change places over the boundary, and their experts that could
             // be among the ones that count
             const float tol = 2 * p.group_top * eta;
@@ -306,25 +372,7 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
     // (equal exact logits without a bias have equal scores: a tie)
     const bool tie = close && delta == 0.0f && !p.bias && my_q == below && below_e >= 0 && sl[my_e] == sl[below_e];
     if (!__any_sync(0xffffffffu, close && !tie)) return kRouteCertain;
-    if (!p.sigmoid && p.bias) {
-        // eta holds for the largest possible score, but the errors are in proportion to the scores
-        // (2.3 delta of the logits and the denominator, fp32's 2^-17 and that of the argument): is
-        // every rank clear of the next by its own, and the last of all that is left?  (Without this
-        // 8192 tokens of 4096 x 256 with a bias took 322 us)
-        auto err = [&](int e) {
-            const float d = mx - sl[e];
-            return (2.3f * delta + 0x1p-17f + d * 0x1p-22f) * __expf(-d) * inv + cmax * 0x1p-22f;
-        };
-        const float c = key32_value(my_q), own = err(my_e);
-        const float next_c = __shfl_down_sync(0xffffffffu, c, 1), next_own = __shfl_down_sync(0xffffffffu, own, 1);
-        bool near = lane < p.k - 1 && c - next_c <= own + next_own;
-        const float low = last - __shfl_sync(0xffffffffu, own, p.k - 1);
-        for (int e = lane; e < p.E; e += 32) {
-            const unsigned v = sk[e];
-            if (v > kMaskedKey32 && key32_value(v) + eta >= low) near |= key32_value(v) + err(e) >= low;
-        }
-        if (!__any_sync(0xffffffffu, near)) return kRouteCertain;
-    }
+    if (sharp && route_ranks_clear(errors, p.E, p.k, lane, my_e, my_q, eta)) return kRouteCertain;
     const unsigned links = __ballot_sync(0xffffffffu, close);   // bit i: ranks i and i + 1 may change places
     // every rank of a link, and what may come up from below the last rank
     int n = p.k;

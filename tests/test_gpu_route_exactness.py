@@ -81,3 +81,50 @@ def test_nan_bias_ranks_last_and_keeps_the_score_as_weight(m, T, score):
         # logits of more than 32 tokens: 2^-17 |x| |W_e|, four times that in a renormalised weight
         dl = 2.0 ** -17 * np.linalg.norm(x.double().numpy(), axis=1)[:, None] * float(wr.double().norm(dim=1).max())
         assert np.all(np.abs(gw - rw) <= rw * (4 * dl + 2.0 ** -23))
+
+
+# ------------------------------------------------------------------ what the tensor cores cut
+
+@pytest.mark.parametrize("H,at", [(128, 5), (2048, 700)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_choice_when_a_token_and_a_row_share_one_large_channel(m, H, at, sign):
+    """A product of 300 in an MMA's sum cuts every product below 2^-17 (25 bits below the largest's
+    exponent): row 0's 127 others, of just less, are lost, and 2^-10 with them."""
+    T, E = 40, 4
+    x = torch.zeros((T, H))
+    lo = at // 128 * 128
+    x[:, lo:lo + 128] = 1.0
+    x[:, at] = 300.0
+    wr = torch.zeros((E, H))
+    wr[0, lo:lo + 128] = sign * 1.9921875 * 2.0 ** -18
+    wr[1, lo + 127] = sign * 1.5 * 2.0 ** -11
+    wr[3, lo + 126] = sign * 1.25 * 2.0 ** -11
+    wr[:, at] = 1.0
+    x, wr = x.bfloat16(), wr.bfloat16()
+    l = x.double().numpy() @ wr.double().numpy().T
+    for kw in (dict(score="softmax"), dict(score="softmax", n_group=2, topk_group=1, group_top=1)):
+        for b in (None, torch.zeros(E)):
+            assert np.array_equal(grouped(m, x, wr, b, 2, **kw)[0], choose(l, 2, **kw)[0])
+
+
+@pytest.mark.parametrize("H", [128, 1000, 4096])
+@pytest.mark.parametrize("outlier", [1.0, 40.0, 3000.0])
+def test_choice_between_close_rows_of_tokens_with_outliers(m, H, outlier):
+    """Channels that are large in x and in W_r; rows in fours that differ in their smallest elements."""
+    g = torch.Generator().manual_seed(H)
+    T, E = 300, 32
+    x, wr = torch.randn((T, H), generator=g).abs(), torch.randn((E, H), generator=g).abs() * 0.5 / H ** 0.5
+    x[:, 3] *= outlier
+    wr[:, 3] = 8.0 / outlier
+    x, wr = x.bfloat16(), wr.bfloat16()
+    for e in range(0, E, 4):
+        for j in range(1, 4):
+            wr[e + j] = wr[e]
+            hit = torch.rand(H, generator=g) < 0.5
+            hit[3] = False
+            # a neighbouring bf16 value
+            wr[e + j, hit] = (wr[e + j, hit].view(torch.int16) + (1 if j % 2 else -1)).view(torch.bfloat16)
+    xd, wd = x.double().numpy(), wr.double().numpy()
+    l = np.stack([(xd * row).sum(1) for row in wd], 1)
+    for kw in (dict(score="softmax"), dict(score="sigmoid", n_group=8, topk_group=3, group_top=2)):
+        assert np.array_equal(grouped(m, x, wr, None, 6, **kw)[0], choose(l, 6, **kw)[0])
