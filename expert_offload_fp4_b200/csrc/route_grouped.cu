@@ -245,6 +245,20 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
+// A row's sum of squares, with what its squares may have lost below the normal range (2^-126 each;
+// they are bf16 or fp32) where that is not small beside the sum.  A row of zeros keeps its 0, which
+// says that its logits are exact: so the row is looked at, by the whole warp.
+__device__ __forceinline__ float with_lost_squares(float sum, const uint4* row, int H, int lane) {
+    const float lost = H * 0x1p-126f;
+    if (!(sum < lost * 0x1p16f)) return sum;
+    uint32_t any = 0;
+    for (int c = lane; c < H / 8; c += 32) {
+        const uint4 q = __ldg(row + c);
+        any |= q.x | q.y | q.z | q.w;
+    }
+    return __any_sync(0xffffffffu, (any & 0x7FFF7FFFu) != 0) ? sum + lost : sum;
+}
+
 // One CTA: 128 tokens x N experts over Kc of H.  Warp 0 loads (TMA, 128-byte swizzle), warp 1
 // issues the MMAs into two accumulators in turn, a chunk of K each; warps 4-11 add the chunks up
 // in registers (a row and 128 experts a thread), after the sums of squares of a share of W_r;
@@ -304,6 +318,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             }
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            sum = with_lost_squares(sum, row, g.H, lane);
             if (lane == 0) g.wn[e] = sum;
         }
     };
@@ -612,6 +627,7 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
         float wmax = 0.0f;
 #pragma unroll
         for (int i = 0; i < kGemmTokens; i++) wmax = max_or_nan(wmax, sh.w2[i]);
+        xn = with_lost_squares(xn, reinterpret_cast<const uint4*>(x + size_t(t) * g.H), g.H, lane);
         delta = (float)(1.02 * (kGemmError * sqrt((double)xn * (double)wmax) +
                                  0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
         if (!(delta <= 0.05f)) mode = kAll;

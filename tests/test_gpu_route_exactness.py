@@ -128,3 +128,43 @@ def test_choice_between_close_rows_of_tokens_with_outliers(m, H, outlier):
     l = np.stack([(xd * row).sum(1) for row in wd], 1)
     for kw in (dict(score="softmax"), dict(score="sigmoid", n_group=8, topk_group=3, group_top=2)):
         assert np.array_equal(grouped(m, x, wr, None, 6, **kw)[0], choose(l, 6, **kw)[0])
+
+
+# ------------------------------------------------------------------ squares out of range
+
+@pytest.mark.parametrize("ex,ew", [(0, 0), (60, 50), (68, 63), (-50, -60), (-63, -68), (-40, -75)])
+def test_choice_of_tokens_whose_squares_leave_the_range(m, ex, ew):
+    """Tokens times 2^-ex and rows times 2^ew.  A token and the rows share one large channel; row 0's
+    127 other products are small enough to be lost beside it, row 1's is not, and row 0 is the larger."""
+    T, E, H = 40, 4, 128
+    x, wr = torch.full((T, H), 2.0 ** -8), torch.zeros((E, H))
+    x[:, 5] = 1.171875
+    wr[0] = 1.9921875 * 2.0 ** -18
+    wr[1, 127] = 1.5 * 2.0 ** -11
+    wr[3, 126] = 1.25 * 2.0 ** -11
+    wr[:, 5] = 1.0
+    xs, ws = (x.double() * 2.0 ** -ex).bfloat16(), (wr.double() * 2.0 ** ew).bfloat16()
+    l = xs.double().numpy() @ ws.double().numpy().T
+    assert np.array_equal(l, (x.double().numpy() @ wr.double().numpy().T) * 2.0 ** (ew - ex))
+    kw = dict(score="softmax")
+    assert np.array_equal(grouped(m, xs, ws, None, 2, **kw)[0], choose(l, 2, **kw)[0])
+
+
+def test_zero_and_tiny_tokens_among_others(m):
+    """Rows of a padded batch, tokens of the smallest elements and of one element."""
+    T, E, H = 130, 40, 264
+    g = torch.Generator().manual_seed(6)
+    x, wr = torch.randn((T, H), generator=g), torch.randn((E, H), generator=g) * 0.1
+    x[::3] = 0
+    x[1::6] = 0
+    x[1::6, 7] = 2.0 ** -133
+    x[5] *= 2.0 ** -126
+    x[8] = -0.0
+    wr[20:] = wr[:20]
+    x, wr = x.bfloat16(), wr.bfloat16()
+    xd, wd = x.double().numpy(), wr.double().numpy()
+    l = np.stack([(xd * row).sum(1) for row in wd], 1)
+    for b in (None, torch.linspace(-0.1, 0.1, E)):
+        for kw in (dict(score="sigmoid"), dict(score="softmax", n_group=8, topk_group=3, group_top=2, renormalize=False)):
+            gi, _ = grouped(m, x, wr, b, 6, **kw)
+            assert np.array_equal(gi, choose(l, 6, bias=None if b is None else b.numpy(), **kw)[0])
