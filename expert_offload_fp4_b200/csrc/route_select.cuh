@@ -104,9 +104,7 @@ enum RouteStatus {
 struct RouteClose {
     int n = 0, e = 0;
     unsigned kept = 0;   // the groups that are certainly kept, in route_fast's form
-    float c = 0.0f;      // selection value (by_logit: the logit)
-    bool want = false;   // it has to be known exactly
-    bool by_logit = false;
+    bool want = false;   // its logit has to be known exactly
 };
 
 // A warp's best expert by 32-bit keys, taken out of sk; each lane keeps the best of its experts
@@ -226,19 +224,25 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
     const float* sl = s.l32;
     unsigned* sk = s.key32;
     bool odd = delta > 0.05f;              // also NaN and infinities: left to the 64-bit way
+    bool small = false;
     unsigned m = 0;
 #pragma unroll 4
     for (int e = lane; e < p.E; e += 32) {
         const float l = sl[e];
         m = max(m, order_key32(l));
         odd |= !(l < INFINITY);
+        small |= l != 0.0f && fabsf(l) < 0x1p-18f;
     }
     mx = key32_value(__reduce_max_sync(0xffffffffu, m));
     odd |= mx == -INFINITY;
-    // Without a bias scores order as the logits do: no score is needed for the choice, as long
-    // as fp64 scores differ wherever fp32 logits do
+    // Without a bias scores order as the logits do: no score is needed for the choice, as long as fp64
+    // scores differ wherever fp32 logits do.  Two logits have one score if they are within about
+    // 2^-52 (2 + e^l) of each other (sigmoid), or 2^-53 of the distance to the largest, or of 1 (softmax);
+    // different fp32 values of 2^-18 or more are 2^-42 apart and 2^-24 of themselves, which is above
+    // that up to 20 (sigmoid), and for the distances to 600 that are let through below (softmax)
     const bool grouped = p.topk_group < p.n_group;
-    const bool by_logit = !p.bias && (!grouped || p.group_top == 1) && (!p.sigmoid || mx <= 20.0f);
+    const bool by_logit = !p.bias && (!grouped || p.group_top == 1) && (!p.sigmoid || mx <= 20.0f) &&
+                          !__any_sync(0xffffffffu, small);
     float inv = 1.0f;
     if (!p.sigmoid && p.bias) {
         float sum = 0.0f;
@@ -269,7 +273,8 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
     // denominator), and of adding the bias
     float eta;
     if (by_logit) {
-        eta = delta;
+        // (logits that are not exact: with what may make one score of two)
+        eta = delta == 0.0f ? 0.0f : delta + (p.sigmoid ? 0x1p-51f * (2.0f + __expf(mx)) : 0x1p-41f);
     } else {
         cmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cmax)));
         eta = (p.sigmoid ? 0.26f * delta + 0x1p-20f : p.bias ? (2.3f * delta + 0x1p-17f) * inv : 1.1f * delta + 0x1p-19f) +
@@ -336,7 +341,6 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
             close_out.n = n;
             close_out.kept = kept & ~open;
             close_out.want = lane < n;
-            close_out.by_logit = by_logit;
             return kRouteGroups;
         }
         // take the other groups out
@@ -381,21 +385,13 @@ __device__ __forceinline__ RouteStatus route_fast(const RouteScratch& s, const R
         for (int i = 0; i < p.E; i += 32) {
             const unsigned v = i + lane < p.E ? sk[i + lane] : 0;
             unsigned h = __ballot_sync(0xffffffffu, v != 0 && v >= near);
-            for (; h; h &= h - 1, n++) {       // one a lane, from lane k on
-                const int src = __ffs(h) - 1;
-                const unsigned q = __shfl_sync(0xffffffffu, v, src);
-                if (lane == n) {
-                    my_e = i + src;
-                    my_q = q;
-                }
-            }
+            for (; h; h &= h - 1, n++)         // one a lane, from lane k on
+                if (lane == n) my_e = i + __ffs(h) - 1;
         }
         if (n > 32) return kRouteOpen;
     }
     close_out.n = n;
     close_out.e = my_e;
-    close_out.c = key32_value(my_q);
-    close_out.by_logit = by_logit;
     close_out.want = lane < p.k ? ((links >> lane) & 1u) || (lane > 0 && ((links >> (lane - 1)) & 1u)) : lane < n;
     return kRouteClose;
 }
@@ -599,10 +595,9 @@ __device__ __noinline__ double route_first_values(const RouteScratch s, const Ro
 // clear `sure`.
 __device__ __noinline__ int route_settle(const RouteScratch s, const RouteChoice& p, const RouteClose& close, double mx,
                                          double inv, double eps, int lane, bool& sure) {
-    double v = close.c, score = 0.0;
-    if (close.want) {
-        const double l = s.l[close.e];
-        score = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv;
+    double v = -INFINITY, score = 0.0;
+    if (lane < close.n && s.l[close.e] != -INFINITY) {
+        score = route_score64(s.l[close.e], p.sigmoid, mx) * inv;
         v = score + (p.bias ? (double)__ldg(p.bias + close.e) : 0.0);
     }
     const unsigned long long key = lane < close.n ? order_key(v) : 0;
@@ -634,8 +629,7 @@ __device__ __noinline__ unsigned route_settle_groups(const RouteScratch s, const
     const int gs = p.E / p.n_group, g = close.want ? close.e / gs : -1;
     double v = 0.0;
     if (close.want) {
-        const double l = s.l[close.e];
-        v = close.by_logit ? l : route_score64(l, p.sigmoid, mx) * inv;
+        v = route_score64(s.l[close.e], p.sigmoid, mx) * inv;
         v += p.bias ? (double)__ldg(p.bias + close.e) : 0.0;
     }
     // each group's best (its lane stands for the group) and second best

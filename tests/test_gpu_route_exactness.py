@@ -168,3 +168,54 @@ def test_zero_and_tiny_tokens_among_others(m):
         for kw in (dict(score="sigmoid"), dict(score="softmax", n_group=8, topk_group=3, group_top=2, renormalize=False)):
             gi, _ = grouped(m, x, wr, b, 6, **kw)
             assert np.array_equal(gi, choose(l, 6, bias=None if b is None else b.numpy(), **kw)[0])
+
+
+# ------------------------------------------------------------------ scores that tie
+
+TIES = [dict(), dict(n_group=4, topk_group=2, group_top=1)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kw", TIES)
+@pytest.mark.parametrize("top", [0.0, 3.0, 15.0])
+@pytest.mark.parametrize("E", [8, 64])
+def test_select_ties_are_those_of_the_scores(m, score, kw, top, E):
+    """Logits near 0 that differ by less than a score's rounding: the lower index, with a bias of
+    zeros as without one."""
+    rng = np.random.default_rng(E)
+    rows = np.zeros((40, E), np.float32)
+    rows[0, :7] = [1e-20, 2e-20, 3e-20, 0, 0, 0, 5e-20]
+    for t in range(1, 40):
+        rows[t] = rng.standard_normal(E) * 10.0 ** rng.choice([-30, -28, -26, -7, -5, -4], E)
+        rows[t, rng.integers(0, E, 3)] = 0
+    if top:
+        rows[:, E - 2] = top
+    l = torch.from_numpy(rows)
+    ri, rw = choose(l.double().numpy(), 3, score=score, **kw)
+    for b in (None, torch.zeros(E)):
+        gi, gw = select(m, l, b, 3, score=score, **kw)
+        assert np.array_equal(gi, ri)
+        assert np.all(np.abs(gw - rw) <= rw * 2.0 ** -23)
+    assert ri[0].tolist()[:2] != [6, 2]
+
+
+@pytest.mark.parametrize("T", [1, 20, 33, 300])
+@pytest.mark.parametrize("kw", TIES)
+def test_ties_of_scores_of_exact_logits(m, T, kw):
+    """Logits from x and W_r: 1e-20 steps beside a largest of 3, and 6e-11 steps at 15, where a
+    sigmoid has no bits for them."""
+    E, H = 16, 64
+    x = torch.zeros((T, H))
+    x[:, 0], x[:, 1], x[:, 2] = 2.0 ** -40, 2.0 ** -17, 1.0
+    near = torch.zeros((E, H))
+    near[:, 0] = 2.0 ** -27 * torch.arange(E).flip(0)
+    near[9, 2] = 3.0
+    high = torch.zeros((E, H))
+    high[:, 1] = 2.0 ** -17 * torch.arange(E)
+    high[:, 2] = 15.0
+    for wr, scores in ((near, ("softmax", "sigmoid")), (high, ("sigmoid",))):
+        x, wr = x.bfloat16(), wr.bfloat16()
+        l = x.double().numpy() @ wr.double().numpy().T
+        for score in scores:
+            for b in (None, torch.zeros(E)):
+                assert np.array_equal(grouped(m, x, wr, b, 5, score=score, **kw)[0], choose(l, 5, score=score, **kw)[0])
