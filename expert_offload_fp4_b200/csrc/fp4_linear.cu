@@ -711,7 +711,7 @@ static int check_weight(const moe_fp4_weight* w) {
 }
 
 // The digits of x, 4 bytes an element of a token pair's columns, fill at most 128 KiB of each of a
-// cluster's 8 CTAs.
+// cluster's 8 CTAs, and up to a stage of every token more where K does not divide evenly.
 static int check_tokens(int T, int K) {
     if (T <= 0 || T > kMaxDecodeT) return fail(MOE_EINVAL, "fp4: T must be in [1, 16]");
     const long long Tp = (T + 1) & ~1;
@@ -778,17 +778,19 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     // (0.3).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9; an
     // exchange of 0.5 has one CTA a tile at 131072 x 4096 for one token: 56.4 us, not 51.3.  Over
     // 120 sizes the choice is 1.1 % above the best C on average, 11 % at most.
-    // At most 128 KiB of digits, so that four stages fit beside them
+    // At most 128 KiB of digits, so that four stages fit beside them; only where no cluster does with
+    // that, up to a stage of every token more (140 KiB at most: three stages fit)
     int bestC = 0;
     long long best = 0;
-    for (int C = 1; C <= kLinMaxCluster && C <= KTall; C++) {
-        const int kt = (KTall + C - 1) / C;
-        if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
-        if (4 * Tp * kt * kLinKT > 128 * 1024) continue;
-        const int ncl = std::min(a.tiles, active[C]), rounds = (a.tiles + ncl - 1) / ncl;
-        const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 6 * rounds;
-        if (!bestC || cost < best) { best = cost; bestC = C; }
-    }
+    for (int cap = 128 * 1024; !bestC && cap <= 128 * 1024 + 4 * Tp * kLinKT; cap += 4 * Tp * kLinKT)
+        for (int C = 1; C <= kLinMaxCluster && C <= KTall; C++) {
+            const int kt = (KTall + C - 1) / C;
+            if ((KTall + kt - 1) / kt != C) continue;   // a CTA without work
+            if (4 * Tp * kt * kLinKT > cap) continue;
+            const int ncl = std::min(a.tiles, active[C]), rounds = (a.tiles + ncl - 1) / ncl;
+            const long long cost = 20LL * rounds * kt + 3 * Tp * kt + 6 * rounds;
+            if (!bestC || cost < best) { best = cost; bestC = C; }
+        }
     if (!bestC) return fail(MOE_EINVAL, "fp4: K too large for this many tokens");
     a.C = bestC;
     const int kt = (KTall + a.C - 1) / a.C;
