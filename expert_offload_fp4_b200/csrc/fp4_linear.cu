@@ -729,13 +729,18 @@ static int check_rows(const void* p, int type, long long ld, int width, int T, c
     return MOE_OK;
 }
 
-// Do the rows of two matrices share any byte?
+// Do the rows of two matrices share any byte?  (Strides are at least a row's length.)
 static bool rows_overlap(const void* a, int a_type, long long lda, int na, const void* b, int b_type, long long ldb, int nb,
                          int T) {
+    const int sa = a_type == MOE_BF16 ? 2 : 4, sb = b_type == MOE_BF16 ? 2 : 4;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    const uintptr_t a1 = a0 + ((T - 1) * lda + na) * (a_type == MOE_BF16 ? 2 : 4);
-    const uintptr_t b1 = b0 + ((T - 1) * ldb + nb) * (b_type == MOE_BF16 ? 2 : 4);
-    return a0 < b1 && b0 < a1;
+    const uintptr_t wa = uintptr_t(na) * sa, wb = uintptr_t(nb) * sb;
+    const uintptr_t pa = uintptr_t(lda) * sa, pb = uintptr_t(ldb) * sb;
+    if (a0 + (T - 1) * pa + wa <= b0 || b0 + (T - 1) * pb + wb <= a0) return false;
+    for (int i = 0; i < T; i++)
+        for (int j = 0; j < T; j++)
+            if (a0 + i * pa < b0 + j * pb + wb && b0 + j * pb < a0 + i * pa + wa) return true;
+    return false;
 }
 
 struct LinDevice {

@@ -92,3 +92,53 @@ def test_k_near_the_limit(m, fmt, T, K, xd):
     # |d silu/dg| <= 1.1; the sigmoid to 2^-21 of its value and its argument's rounding
     b = 1.1 * bg * (np.abs(u) + bu) + silu * bu + silu * np.abs(u) * (2.0 ** -21 + np.abs(g) * 2.0 ** -23) + 1e-37
     assert np.all(np.abs(h.double().cpu().numpy() - g * sg * u) <= b)
+
+
+# ------------------------------------------------------------------ operands in one buffer
+
+@pytest.mark.parametrize("T", [2, 16])
+@pytest.mark.parametrize("yd", [torch.bfloat16, torch.float32])
+def test_column_slices_of_one_buffer(m, T, yd):
+    """x, add and y beside one another in the rows of one buffer; the columns between stay."""
+    N, K = 320, 256
+    Wq, W = weight(m, N, K, "nvfp4", 1)
+    buf = torch.randn((T, K + 8 + 2 * N + 8), generator=torch.Generator().manual_seed(T)).to(yd).cuda()
+    before = buf.clone()
+    x, add, y = buf[:, :K], buf[:, K + 8:K + 8 + N], buf[:, K + 8 + N:K + 8 + 2 * N]
+    st = status()
+    m.fp4_linear(x, Wq, y, st, add=add)
+    torch.cuda.synchronize()
+    xc, ac = before[:, :K].cpu(), before[:, K + 8:K + 8 + N].double().cpu().numpy()
+    ref = xc.double().numpy() @ W.T + ac
+    got = y.double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= bound(xc, W, K, yd, ref) + np.abs(ac) * 2.0 ** -24)
+    assert torch.equal(buf[:, :K + 8 + N], before[:, :K + 8 + N]) and torch.equal(buf[:, K + 8 + 2 * N:], before[:, K + 8 + 2 * N:])
+    assert int(st.item()) == 0
+
+
+def test_rows_dealt_out_in_turn_share_a_buffer(m):
+    """Rows of x and y alternate: their spans cross, their bytes do not."""
+    T, K = 5, 512
+    Wq, W = weight(m, K, K, "mxfp4", 2)
+    buf = acts(2 * T, K, 3).cuda()
+    x, y = buf[0::2], buf[1::2]
+    xc, st = x.cpu(), status()
+    m.fp4_linear(x, Wq, y, st)
+    torch.cuda.synchronize()
+    ref = xc.double().numpy() @ W.T
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= bound(xc, W, K, torch.bfloat16, ref))
+    assert torch.equal(x.cpu(), xc)
+
+
+def test_operands_that_do_share_bytes_are_refused(m):
+    T, K = 4, 256
+    Wq, _ = weight(m, K, K, "nvfp4", 4)
+    buf, st = torch.zeros((T + 1, 2 * K), dtype=torch.bfloat16, device="cuda"), status()
+    flat = buf.view(-1)
+    x = buf[:T, :K]
+    for y in (buf[:T, K - 2:2 * K - 2], buf[:T, 8:K + 8], flat[2 * K - 8:2 * K - 8 + T * 2 * K].view(T, 2 * K)[:, :K],
+              flat[K + 2:K + 2 + 3 * (2 * K - 64) + K].as_strided((T, K), (2 * K - 64, 1))):
+        with pytest.raises(m._lib.MoeError, match="y overlaps x"):
+            m.fp4_linear(x, Wq, y, st)
+        with pytest.raises(m._lib.MoeError, match="y overlaps add"):
+            m.fp4_linear(torch.zeros((T, K), dtype=torch.bfloat16, device="cuda"), Wq, y, st, add=x)
