@@ -715,7 +715,7 @@ static int check_weight(const moe_fp4_weight* w) {
 static int check_tokens(int T, int K) {
     if (T <= 0 || T > kMaxDecodeT) return fail(MOE_EINVAL, "fp4: T must be in [1, 16]");
     const long long Tp = (T + 1) & ~1;
-    if (Tp * ((K + kLinKT - 1) / kLinKT * kLinKT) > 262144)
+    if (Tp * ((K + (kLinKT - 1LL)) / kLinKT * kLinKT) > 262144)
         return fail(MOE_EINVAL, "fp4: K too large for this many tokens (K * T, T rounded up to even, at most 262144)");
     return MOE_OK;
 }

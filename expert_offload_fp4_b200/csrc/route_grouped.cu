@@ -29,6 +29,7 @@ constexpr int kGemmTokens = 4;           // tokens, a warp each, per CTA of the 
 constexpr int kSmallTile = 8;            // largest token tile of the fp64 kernel
 constexpr int kSmallT = 32;              // most tokens it takes
 constexpr size_t kCounterBytes = 256;    // its tickets, at the start of the workspace
+constexpr int kMaxRouteSize = 1 << 30;   // largest T and H: twice that, and their rounding up, stay ints
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
@@ -746,6 +747,7 @@ static int check_choice(const moe_route_choice* c, const float* bias, int T, int
     if (!c) return fail(MOE_EINVAL, "null routing choice");
     if (T <= 0 || E <= 0 || E > kMaxE || c->k <= 0 || c->k > kMaxK)
         return fail(MOE_EINVAL, "grouped route: need T > 0, 0 < E <= 1024, 0 < k <= 32");
+    if (T > kMaxRouteSize) return fail(MOE_EINVAL, "grouped route: T must be at most 2^30");
     if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID)
         return fail(MOE_EINVAL, "grouped route: unknown score");
     if (c->n_group <= 0 || c->n_group > kMaxGroups || E % c->n_group)
@@ -877,7 +879,7 @@ static size_t route_workspace(int T, int E) {
 }
 
 extern "C" size_t moe_route_grouped_workspace_bytes(int T, int E) {
-    if (T <= 0 || E <= 0 || E > kMaxE) return 0;
+    if (T <= 0 || T > kMaxRouteSize || E <= 0 || E > kMaxE) return 0;
     // more tiles of tokens have fewer parts: the most of any number of tiles up to T's
     size_t most = route_workspace(T, E);
     for (int t = 128; t < T && t <= 128 * kRgTargetCtas; t += 128) most = std::max(most, route_workspace(t, E));
@@ -891,7 +893,8 @@ extern "C" int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const 
     const int rc = check_choice(choice, bias, T, E, p);
     if (rc) return rc;
     if (!x_bf16 || !wr_bf16 || !idx || !w) return fail(MOE_EINVAL, "null pointer");
-    if (H <= 0 || H % 8) return fail(MOE_EINVAL, "grouped route: H must be a positive multiple of 8");
+    if (H <= 0 || H % 8 || H > kMaxRouteSize)
+        return fail(MOE_EINVAL, "grouped route: H must be a positive multiple of 8, at most 2^30");
     if ((reinterpret_cast<uintptr_t>(x_bf16) | reinterpret_cast<uintptr_t>(wr_bf16)) & 15)
         return fail(MOE_EINVAL, "grouped route: x and W_r must be 16-byte aligned");
     if (!workspace || workspace_bytes < route_workspace(T, E))

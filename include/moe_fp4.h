@@ -254,7 +254,7 @@ int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias
  * moe_route_grouped_workspace_bytes(T, E) bytes (enough for fewer tokens, too), 256-byte
  * aligned, zeroed before its first use (every call leaves its counters, the first 256
  * bytes, zero); calls that may overlap, and captured graphs that may be replayed at the
- * same time, need one each.  E <= 1024.
+ * same time, need one each.  E <= 1024, T and H at most 2^30.
  * Errors: MOE_EINVAL. */
 size_t moe_route_grouped_workspace_bytes(int T, int E);
 int moe_route_grouped(const void* x_bf16, const void* wr_bf16, const float* bias, int T, int H, int E,
