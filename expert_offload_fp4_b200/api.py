@@ -402,6 +402,12 @@ def decode_layer_routed(pool, layer, x, idx, w, slot_of, y_part, y, status, look
     idx and w that another router wrote on the same stream."""
     if copy_stream is None:
         raise ValueError("decode_layer_routed needs a copy_stream of its own (torch.cuda.Stream())")
+    T = x.shape[0]
+    _need(idx.dtype == torch.int32 and idx.shape == (T, pool.k) and idx.is_contiguous(),
+          "idx must be a contiguous int32 [T, k], k the pool's")
+    _need(w.dtype == torch.float32 and w.shape == (T, pool.k) and w.is_contiguous(),
+          "w must be a contiguous float32 [T, k], k the pool's")
+    _need(idx.is_cuda and idx.device == w.device == x.device, "x, idx and w must be on one CUDA device")
     ev0, ev1 = (None, None) if copy_events is None else (C.c_void_p(copy_events[0].cuda_event),
                                                         C.c_void_p(copy_events[1].cuda_event))
     L.check("moe_decode_layer_routed", pool.lib.moe_decode_layer_routed(

@@ -36,3 +36,21 @@ def test_sizes_at_the_edge_of_an_int_are_refused(m):
         w = E.Fp4WeightDesc(p, p, 1.0, 64, K, E.MOE_NVFP4)
         refused(b"K too large", L.moe_fp4_linear(C.byref(w), p, E.MOE_BF16, 1 << 40, 1, None, 0, p + 2048, E.MOE_BF16, 64, st, None))
         refused(b"K too large", L.moe_fp4_swiglu(C.byref(w), C.byref(w), p, E.MOE_BF16, 1 << 40, 1, p + 2048, 64, st, None))
+
+
+def test_a_routed_layer_checks_the_choice_it_is_given(m):
+    """idx and w are inputs here: an int64 idx, as torch.topk gives, or another k is not read as int32 [T, k]."""
+    called = []
+    pool = SimpleNamespace(k=2, E=8, H=256, handle=None,
+                           lib=SimpleNamespace(moe_decode_layer_routed=lambda *a: called.append(a) or 0))
+    x = torch.zeros((3, 256), dtype=torch.bfloat16)
+    idx, w = torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2))
+    cs = SimpleNamespace(cuda_stream=1)
+    for what, bad in [("idx", dict(idx=idx.long())), ("idx", dict(idx=idx[:2])), ("idx", dict(idx=torch.zeros((3, 4), dtype=torch.int32))),
+                      ("idx", dict(idx=torch.zeros((3, 4), dtype=torch.int32)[:, ::2])), ("w must", dict(w=w.double())),
+                      ("w must", dict(w=w.bfloat16())), ("w must", dict(w=w[:, :1])), ("w must", dict(w=torch.zeros((2, 3)).t())),
+                      ("CUDA device", {})]:
+        a = dict(idx=idx, w=w) | bad
+        with pytest.raises(ValueError, match=what):
+            m.decode_layer_routed(pool, 0, x, a["idx"], a["w"], None, None, None, None, copy_stream=cs, stream=cs)
+    assert not called
