@@ -16,13 +16,16 @@ from . import api
 
 
 class DecodeLayer:
-    """router: None for moe_route's gate (softmax over the chosen or over all experts), or
-    an api.GroupedRouting: sigmoid or softmax scores, the bias steering only the choice,
-    groups of experts."""
+    """router: None for moe_route's gate (softmax over the chosen experts, or with
+    renormalize=0 over all), or an api.GroupedRouting, which has a renormalize of its own:
+    sigmoid or softmax scores, the bias steering only the choice, groups of experts."""
 
-    def __init__(self, pool: api.Pool, T: int, device="cuda", renormalize=1, overlap=True, router=None):
+    def __init__(self, pool: api.Pool, T: int, device="cuda", renormalize=None, overlap=True, router=None):
         if T > pool.max_tokens:
             raise ValueError("T exceeds the pool's max_tokens")
+        if router is not None and renormalize is not None:
+            raise ValueError("renormalize is moe_route's: with a router, set its own")
+        renormalize = 1 if renormalize is None else renormalize
         self.router = router
         self._options = None if router is None else asdict(router)
         self._h = []         # the shared expert's hidden activations: the last is the largest

@@ -54,3 +54,11 @@ def test_a_routed_layer_checks_the_choice_it_is_given(m):
         with pytest.raises(ValueError, match=what):
             m.decode_layer_routed(pool, 0, x, a["idx"], a["w"], None, None, None, None, copy_stream=cs, stream=cs)
     assert not called
+
+
+def test_a_layer_with_a_router_of_its_own_refuses_renormalize(m):
+    """renormalize belongs to moe_route's gate; a GroupedRouting has its own."""
+    pool = SimpleNamespace(k=2, E=8, H=256, max_tokens=4)
+    for r in (0, 1):
+        with pytest.raises(ValueError, match="renormalize"):
+            m.DecodeLayer(pool, 2, device="cpu", router=m.GroupedRouting(), renormalize=r)
