@@ -19,6 +19,8 @@
 #include "tcgen05.cuh"
 #include "route_select.cuh"
 
+#include <atomic>
+
 namespace moe {
 
 int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
@@ -764,13 +766,13 @@ static int check_choice(const moe_route_choice* c, const float* bias, int T, int
 
 // Raise a kernel's shared-memory limit, once per device.
 template <typename Kern>
-static cudaError_t raise_smem(Kern kern, int bytes, bool (&done)[64]) {
+static cudaError_t raise_smem(Kern kern, int bytes, std::atomic<bool> (&done)[64]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
@@ -787,7 +789,7 @@ struct RouteCall {
 template <int TT>
 static cudaError_t launch_small(const RouteCall& r) {
     auto kern = grouped_small_kernel<TT>;
-    static bool done[64] = {};
+    static std::atomic<bool> done[64] = {};
     cudaError_t e = raise_smem(kern, (int)(kSmallTile * RouteScratch::bytes(kMaxE)), done);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((r.p.E + 1) / 2, (r.T + TT - 1) / TT), dim3(kChooseWarps * 32),
@@ -820,7 +822,7 @@ static int launch_large(const RouteCall& r) {
     int rc;
     if ((rc = make_tmap_2d(&mx, r.x, size_t(r.H) * 2, r.T, size_t(r.H) * 2, 128, 128, true))) return rc;
     if ((rc = make_tmap_2d(&mw, r.wr, size_t(r.H) * 2, E, size_t(r.H) * 2, 128, g.N, true))) return rc;
-    static bool gdone[64] = {}, cdone[2][64] = {};
+    static std::atomic<bool> gdone[64] = {}, cdone[2][64] = {};
     // (the sums leave through 2 x 128 half rows of 528 bytes)
     const int smem = std::max(kRgStages * (16384 + g.N * 128), 256 * 528) + 1024;
     MOE_CUDA_TRY(raise_smem(route_gemm_kernel, kRgStages * (16384 + kRgMaxN * 128) + 1024, gdone));
@@ -845,7 +847,7 @@ static int launch_grouped(const RouteCall& r) {
 static int launch_select(const void* logits, int bf16, long long ld, int T, const RouteChoice& p, int32_t* idx, float* w,
                          cudaStream_t s) {
     auto kern = route_select_kernel;
-    static bool done[64] = {};
+    static std::atomic<bool> done[64] = {};
     MOE_CUDA_TRY(raise_smem(kern, (int)(kChooseWarps * RouteScratch::bytes(kMaxE)), done));
     MOE_CUDA_TRY(launch_pdl(kern, dim3((T + kChooseWarps - 1) / kChooseWarps), dim3(kChooseWarps * 32),
                             kChooseWarps * RouteScratch::bytes(p.E), s, logits, bf16, ld, T, p, idx, w));
