@@ -142,3 +142,23 @@ def test_operands_that_do_share_bytes_are_refused(m):
             m.fp4_linear(x, Wq, y, st)
         with pytest.raises(m._lib.MoeError, match="y overlaps add"):
             m.fp4_linear(torch.zeros((T, K), dtype=torch.bfloat16, device="cuda"), Wq, y, st, add=x)
+
+
+# ------------------------------------------------------------------ tokens on their own
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("T,N,K", [(2, 200, 512), (5, 700, 2048), (16, 1000, 4096)])
+def test_a_token_does_not_see_the_others(m, fmt, T, N, K):
+    """The same token at the same place among others, huge, tiny, zero and NaN ones included: the same bits."""
+    Wq, _ = weight(m, N, K, fmt, 5)
+    x = acts(T, K, 6)
+    out = []
+    for i, s in enumerate((1.0, 2.0 ** 90, 2.0 ** -90, 0.0, float("nan"))):
+        other = (acts(T, K, 7 + i).float() * s).bfloat16()
+        other[T // 2] = x[T // 2]
+        y, st = torch.empty((T, N), device="cuda"), status()
+        m.fp4_linear(other.cuda(), Wq, y, st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        out.append(y[T // 2].cpu())
+    assert all(torch.equal(o, out[0]) for o in out) and torch.isfinite(out[0]).all()

@@ -219,3 +219,23 @@ def test_ties_of_scores_of_exact_logits(m, T, kw):
         for score in scores:
             for b in (None, torch.zeros(E)):
                 assert np.array_equal(grouped(m, x, wr, b, 5, score=score, **kw)[0], choose(l, 5, score=score, **kw)[0])
+
+
+# ------------------------------------------------------------------ weights of few tokens
+
+@pytest.mark.parametrize("T,H,E,k,kw,with_bias", [
+    (1, 4096, 256, 6, dict(score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5), True),
+    (3, 2048, 128, 8, dict(score="softmax", renormalize=False, scale=16.0), False),
+    (8, 264, 20, 3, dict(score="softmax", n_group=5, topk_group=2, group_top=2), True),
+    (32, 4096, 384, 8, dict(score="sigmoid", renormalize=False), True),
+    (17, 512, 1024, 32, dict(score="softmax", n_group=32, topk_group=9, group_top=1), True)])
+def test_weights_of_few_tokens_are_rounded_once(m, T, H, E, k, kw, with_bias):
+    """Up to 32 tokens the logits are fp64 sums of exact products, off by less than 2^-40 of 1 here; a weight
+    is one rounding (2^-24) from the 64-bit one."""
+    g = torch.Generator().manual_seed(T + E)
+    x, wr = torch.randn((T, H), generator=g).bfloat16(), (torch.randn((E, H), generator=g) * 0.9 / H ** 0.5).bfloat16()
+    b = (torch.rand(E, generator=g) - 0.5) * 0.2 if with_bias else None
+    gi, gw = grouped(m, x, wr, b, k, **kw)
+    ri, rw = choose(x.double().numpy() @ wr.double().numpy().T, k, bias=None if b is None else b.numpy(), **kw)
+    assert np.array_equal(gi, ri)
+    assert np.all(np.abs(gw - rw) <= rw * (2.0 ** -24 + 2.0 ** -38))
