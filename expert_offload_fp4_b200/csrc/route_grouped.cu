@@ -535,10 +535,10 @@ __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, co
     __syncthreads();
 }
 
-// One warp per token.  Five CTAs on an SM leave 96 registers a thread (so exact_logits has half the
-// loads in flight: with as many it spills, and a softmax with a bias takes 403 us, not 331), which pays
-// where there are many: 8192 tokens of 4096 x 256 take 66.5 us with five and 70.0 with four, but
-// 2048 of 2048 x 128 take 23.4 and 22.4.
+// One warp per token.  Five CTAs on an SM leave 96 registers a thread, so that exact_logits has half the
+// loads in flight (with as many it spills).  That pays where there are many tokens, most of which need no
+// exact logit: 16384 tokens of 4096 x 256 take 126 us with five and 129 with four, 8192 of 2048 x 128 48.3 and
+// 50.4, but 2048 of 2048 x 128 25.8 and 24.6, and 8192 of 4096 x 256 with a softmax and a bias 547 and 422.
 template <int kCtas>
 __global__ void __launch_bounds__(kGemmTokens * 32, kCtas)
 route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, RouteGemmArgs g, RouteChoice p,
@@ -829,7 +829,8 @@ static int launch_large(const RouteCall& r) {
     const dim3 grid(((r.T + 127) / 128) * g.n_tiles * g.split);
     MOE_CUDA_TRY(launch_pdl(route_gemm_kernel, grid, dim3(kRgThreads), smem, r.s, mx, mw, g));
     const int ctas = (r.T + kGemmTokens - 1) / kGemmTokens;
-    const bool many = ctas > 8 * kRgTargetCtas;            // more than two rounds of four an SM
+    // more than two rounds of four an SM; a softmax with a bias asks for the most exact logits
+    const bool many = ctas > 8 * kRgTargetCtas && (r.p.sigmoid || !r.p.bias);
     auto kern = many ? route_gemm_choose_kernel<5> : route_gemm_choose_kernel<4>;
     MOE_CUDA_TRY(raise_smem(kern, (int)(kGemmTokens * RouteScratch::bytes(kMaxE)), cdone[many]));
     MOE_CUDA_TRY(launch_pdl(kern, dim3(ctas), dim3(kGemmTokens * 32), kGemmTokens * RouteScratch::bytes(E), r.s, r.x, r.wr,
