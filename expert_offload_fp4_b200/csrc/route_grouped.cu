@@ -204,23 +204,28 @@ constexpr int kRgMaxN = 256;             // experts per CTA
 constexpr int kRgTargetCtas = 148;
 constexpr int kRgChunk = 2;              // stages (64 elements each) the tensor core sums by itself
 
-// Error of the tensor core's sums over |x_t| |W_e|.  What an MMA step does here, seen by sums of
-// powers of two at every place: it cuts its 16 products and the accumulator towards zero at the 25th
-// binary place below the largest exponent among them, adds them, and cuts the sum to 24 bits.  Let M
-// bound the sizes of all partial sums of a chunk and of its products: |x| |W| of the chunk does.  The
-// largest term loses nothing, so a step loses less than 16 2^-25 M (the chunk's first 15 2^-25 M) and
-// 2^-23 M for the sum: (20 n - 1) 2^-25 M in the n = 8 steps of a chunk, and the chunks' bounds add up
-// to as much of |x| |W|.  (One product of 1 before 127 of just under 2^-24 comes within a fifth of it;
-// dense rows err by 2^-21.9 of |x| |W| where all products are positive, 2^-23.6 of random sign.)  The
-// chunks are added in fp32 registers: 2^-24 of the largest sum each.
-constexpr double kGemmError = (20 * 4 * kRgChunk - 1) * 0x1p-25;
+// Error of the tensor core's sums.  What an MMA step does here, seen by sums of powers of two at every
+// place: it cuts its 16 products and the accumulator towards zero at the 25th binary place below the
+// largest exponent among them, adds them, and cuts the sum to 24 bits.  The largest term loses nothing,
+// so step s loses less than 16 2^-25 M_s, M_s its largest product or the accumulator before it, and
+// 2^-23 of its sum.  Let q_s be the sum of the sizes of its products, S that of all n steps of a chunk
+// (at most the chunk's |x| |W|), V the size of the chunk's sum, as it is read out, and h = (S + V) / 2.
+// The accumulator before step s is at most q_1 + .. + q_(s-1), and at most V + q_s + .. + q_n: at most h.
+// So all M_s are at most h, but for one whose q_s is above h, and then the others are at most 2 h - q_s:
+// their sum is at most n h.  Altogether 2^-25 times 16 n h + 4 (n - 1) h + 4 V, and the chunks' S add up
+// to |x| |W| at most.  (One product of 1 before 127 of just under 2^-24 loses 2^-18 of |x| |W|, a
+// fifth less than this allows; dense rows 2^-21.9 where all products are positive, 2^-23.6 of random
+// sign.)  The chunks are added in fp32 registers: 2^-24 of at most the sum of all V each.
+constexpr int kChunkSteps = 4 * kRgChunk;
+constexpr double kErrorS = (8 * kChunkSteps + 2 * (kChunkSteps - 1)) * 0x1p-25;
+constexpr double kErrorV = kErrorS + 4 * 0x1p-25;
 
 struct RouteGemmArgs {
     int T, H, E, Ep;          // Ep: row length of the partial logits
     int n_tiles, N, split, Kc;
     float* part;              // [split][T][Ep]
     float* xn;                // [split][T] sums of squares of x
-    float* xm;                // [split][n_tiles][T] largest sum of a row
+    float* xm;                // [split][n_tiles][T] sum over the chunks of a row's largest chunk sum
     float* wn;                // [E] sums of squares of W_r
     const uint16_t* wr;
     unsigned long long limit_ns;
@@ -275,7 +280,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[kRgStages], empty[kRgStages], accf[2], acce[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ unsigned s_max[128];      // largest |sum| per row (float bits)
+    __shared__ unsigned s_max[128];      // the rows' xm (float bits)
     __shared__ float s_sq[128];          // sums of squares of the rows
     __shared__ int s_bad;                // a wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -410,6 +415,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             __syncwarp();
             tc_fence_after();
             const uint32_t acc = tbase + (j & 1) * g.N + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
+            float most = 0.0f;
 #pragma unroll
             for (int b = 0; b < 8; b++) {
                 if (16 * b >= width) break;
@@ -418,9 +424,10 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     add_f32x2(sum[b][i], sum[b][i + 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                    top = fmaxf(fmaxf(top, fabsf(sum[b][i])), fabsf(sum[b][i + 1]));
+                    most = fmaxf(fmaxf(most, fabsf(__uint_as_float(v[i]))), fabsf(__uint_as_float(v[i + 1])));
                 }
             }
+            top += most;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acce[j & 1]);
@@ -573,8 +580,8 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
     }
     if (t < g.T) {
         if (lane < g.split) xn = __ldg(g.xn + (size_t)lane * g.T + t);
-        // (the sum over the tiles of experts is more than their largest)
-        for (int c = lane; c < g.split * g.n_tiles; c += 32) xm += __ldg(g.xm + (size_t)c * g.T + t);
+        if (lane < g.split)
+            for (int i = 0; i < g.n_tiles; i++) xm = max_or_nan(xm, __ldg(g.xm + (size_t)(lane * g.n_tiles + i) * g.T + t));
         auto put = [&](int e, const float (&l)[4]) {
             float bias[4];
 #pragma unroll
@@ -631,8 +638,9 @@ route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restr
 #pragma unroll
         for (int i = 0; i < kGemmTokens; i++) wmax = max_or_nan(wmax, sh.w2[i]);
         xn = with_lost_squares(xn, reinterpret_cast<const uint4*>(x + size_t(t) * g.H), g.H, lane);
-        delta = (float)(1.02 * (kGemmError * sqrt((double)xn * (double)wmax) +
-                                 0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split) * (double)xm));
+        // (2 % for the norms, which err by 0.4 %, and for the roundings of xm and in these bounds themselves)
+        delta = (float)(1.02 * (kErrorS * sqrt((double)xn * (double)wmax) +
+                                 (kErrorV + 0x1p-24 * (g.Kc / (64 * kRgChunk) + 1 + g.split)) * (double)xm));
         if (!(delta <= 0.05f)) mode = kAll;
         else choose = true;
     }
