@@ -110,8 +110,10 @@ __device__ __forceinline__ double warp_sum_tokens(double (&v)[TT], int lane) {
     return v[0];
 }
 
+// (Two CTAs an SM cover every grid of up to 32 tokens of 256 experts in two rounds, and leave the larger tiles
+// the registers they need: without that they spill, and 16 tokens of 4096 x 256 take 15.6 us, not 12.5)
 template <int TT>
-__global__ void __launch_bounds__(kChooseWarps * 32)
+__global__ void __launch_bounds__(kChooseWarps * 32, TT >= 4 ? 2 : 0)
 grouped_small_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int T, int H, RouteChoice p,
                      int32_t* __restrict__ idx, float* __restrict__ wout, double* __restrict__ logits,
                      unsigned int* __restrict__ tile_cnt) {
