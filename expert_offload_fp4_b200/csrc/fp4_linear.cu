@@ -782,7 +782,7 @@ static int launch_variant(LinArgs& a, const CUtensorMap& m0, const CUtensorMap& 
     // CTA, the conversion of its part of x (0.15 a KiB of digits) and the exchange of each tile
     // (0.3).  Measured against the stages alone: 4096 x 4096 for 16 tokens 9.5 us, not 10.9; an
     // exchange of 0.5 has one CTA a tile at 131072 x 4096 for one token: 56.4 us, not 51.3.  Over
-    // 120 sizes the choice is 1.1 % above the best C on average, 11 % at most.
+    // 200 sizes the choice is 1.1 % above the best C on average, 11 % at most.
     // At most 128 KiB of digits, so that four stages fit beside them; only where no cluster does with
     // that, up to a stage of every token more (140 KiB at most: three stages fit)
     int bestC = 0;

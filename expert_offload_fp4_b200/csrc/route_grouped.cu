@@ -4,18 +4,19 @@
 // cores.  Two experts a CTA, its eight warps over parts of H, so that the few hundred rows
 // of W_r are read by every SM at once; the last CTA of a token tile (a ticket per tile,
 // reset by that CTA) makes the choice, one warp a token.  Latency: for one token of 4096 x 256,
-// 8.5 us (launch and products 2.7, the choice 5.5), which is 2.1 MB at 0.25 TB/s.
+// 9.0 us (launch and products 2.7, the rest the choice), which is 2.1 MB at 0.23 TB/s.
 //
 // Many tokens (a prompt): fp64 would take 100 times the tensor cores' time.  A tcgen05
 // GEMM gives the logits in fp32 together with |x_t| and |W_e|, from which a bound on
 // a logit's error follows; the choice then computes a logit again in fp64, from x and
 // W_r, only where a decision hangs on less than that bound allows (a few tokens in a
 // hundred, a few experts each).  So both ways choose the same experts.  8192 tokens of
-// 4096 x 256 take 66.6 us: the GEMM 23 (17 GFLOP, 0.75 PFLOP/s; its accumulators are read
-// out every 128 of H), the choice 39 (some 2400 instructions a token).  The GEMM's fixed cost
-// makes it the slower way up to 32 tokens: 24 tokens of 4096 x 256 take 18.6 us in fp64 and
-// 20.1 with it, 32 of 2048 x 128 10.2 and 13.3, 32 of 7168 x 256 26.6 and 27.6; 40 tokens
-// 23.7 and 21.6, 12.5 and 13.3, 34.9 and 27.9.
+// 4096 x 256 take 71.5 us: the GEMM 23 (17 GFLOP, 0.75 PFLOP/s; its accumulators are read
+// out every 128 of H), the choice the rest (some 2500 instructions a token).  The GEMM's fixed
+// cost makes it the slower way up to 32 tokens, whose weights are promised to come from exact
+// logits: 24 tokens of 4096 x 256 take 16.0 us in fp64 and 20.6 with it, 32 of 2048 x 128 9.8 and
+// 15.0, 32 of 7168 x 256 22.3 and 25.1; 40 tokens 19.2 and 22.1, 11.3 and 15.4, 25.4 and 25.8; 64 of
+// 4096 x 256 25.2 and 22.5.
 #include "tcgen05.cuh"
 #include "route_select.cuh"
 
@@ -546,8 +547,8 @@ __device__ __noinline__ void exact_logits(ChooseShared& sh, uint8_t* scratch, co
 
 // One warp per token.  Five CTAs on an SM leave 96 registers a thread, so that exact_logits has half the
 // loads in flight (with as many it spills).  That pays where there are many tokens, most of which need no
-// exact logit: 16384 tokens of 4096 x 256 take 126 us with five and 129 with four, 8192 of 2048 x 128 48.3 and
-// 50.4, but 2048 of 2048 x 128 25.8 and 24.6, and 8192 of 4096 x 256 with a softmax and a bias 547 and 422.
+// exact logit: 8192 tokens of 4096 x 256 take 71.5 us with five and 73.2 with four, 8192 of 2048 x 128 47.1 and
+// 49.3, but 2048 of 2048 x 128 25.5 and 24.4, and 8192 of 4096 x 256 with a softmax and a bias 500 and 388.
 template <int kCtas>
 __global__ void __launch_bounds__(kGemmTokens * 32, kCtas)
 route_gemm_choose_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, RouteGemmArgs g, RouteChoice p,

@@ -14,13 +14,13 @@
 // of all experts cost more than all the rest, so the choice is first made in fp32
 // (route_fast), with a bound eta on the values' error (eta also covers the error of
 // logits that come from the tensor cores), and stands if every distance that decided
-// it is above the bounds.  Groups or ranks that are closer are settled by the fp64 values
+// it is above the bounds, eta's or the experts' own (route_groups_clear, route_ranks_clear).  Groups or ranks that are closer are settled by the fp64 values
 // of the few experts they hang on (route_settle_groups, then route_fast again with the
 // groups given; route_settle).  What is left, such as more than 32 such experts, goes
 // through route_attempt: values within their bounds of a decision are computed again in
 // fp64, and the choice is repeated until it stands.  (With every close pair of groups
-// left to route_attempt, the few tokens that have one were a launch's tail: 16 tokens of
-// 4096 x 256 took 15.5 us, not 13.1, and 512 tokens 33.4, not 27.3.)
+// left to route_attempt, the few tokens that have one were a launch's tail: 2.4 us more for
+// 16 tokens of 4096 x 256, 6 for 512.)
 //
 // b_e = -inf masks expert e (as l_e = -inf does): it adds nothing to its group,
 // ranks below every unmasked expert and weighs 0.  A NaN c ranks like a masked

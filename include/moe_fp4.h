@@ -243,6 +243,9 @@ int moe_route_noalloc(const void* x_bf16, const void* wr_bf16, const float* bias
  *   w_j = scale * s_j, divided by the sum of the chosen s if renormalize
  * bias may be NULL; it never enters the weights.  The choice is made on 64-bit
  * values of the exact logits, so it does not depend on T or on the order of sums.
+ * Weights come from exact logits for up to 32 tokens in a call, from fp32 sums of
+ * the tensor cores for more (off by at most 2^-17 |x| |W_e|, by less than 2^-21 of it
+ * where rows are dense).
  * bias_e = -inf masks expert e: it adds nothing to its group's value, ranks below
  * every unmasked expert of the kept groups (then by index) and has weight 0.  A NaN
  * selection value ranks like a masked one; its weight is still that of its score, NaN
@@ -272,8 +275,9 @@ int moe_route_select(const void* logits, int type, long long ld, const float* bi
  * experts (a shared expert, projections, an output head) in the experts' formats:
  *   y[t, n] = add[t, n] + S * sum_k x[t, k] * e2m1(codes[n, k]) * scale[n, k / bs]
  * x [T, K] of x_type (rows 16-byte aligned), y [T, N] of y_type, add NULL or [T, N]
- * of y_type (it may be y itself: y += W x; otherwise no output may overlap an
- * input); row strides ldx, ld_add, ldy in elements.  Sums in fp32, one rounding to
+ * of y_type (it may be y itself: y += W x; otherwise no row of an output may share
+ * bytes with a row of an input); row strides ldx, ld_add, ldy in elements, at least a
+ * row's length.  Sums in fp32, one rounding to
  * y_type at the end; x enters to 2^-22 of its largest element in the token (bf16
  * elements down to 2^-14 of it exactly).  A NaN or infinite element makes all of
  * its token's outputs NaN; so may weights so large (MXFP4 scales above 2^96) that
@@ -478,7 +482,9 @@ int moe_decode_layer_routed(moe_pool* pool, int layer, const void* x_bf16, int T
  * decode FFN launch per layer with the router (the same logits, choices and
  * weights as moe_route, bit for bit), the slot lookup and the combine fused in,
  * on `stream`, with no host wait anywhere, so the call may be captured into a
- * CUDA graph and replayed.  Every expert the
+ * CUDA graph and replayed.  As in moe_expert_ffn, x must be complete before the kernel
+ * ahead of the call on `stream` starts: it may not be what a decode FFN or moe_combine
+ * directly ahead is still writing (any other kernel between is enough).  Every expert the
  * layers touch must already be resident (for instance a pool with
  * n_slots >= L * E after one pass of moe_decode_layer): each expert's slot comes
  * from the pool's key table and the hits' LRU clocks are refreshed exactly as
